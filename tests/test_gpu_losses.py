@@ -1,0 +1,353 @@
+"""The loss operators (zero_loss.h) on the GPU against their definition in
+float64, at the sizes, masks, strides and types where they can go wrong."""
+import math
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():  # pragma: no cover
+    pytest.skip("needs a GPU", allow_module_level=True)
+
+from zero_sharded_optimizer_amd import losses  # noqa: E402
+from loss_cases import DTYPES, check, make, reference  # noqa: E402
+
+
+def say(*a):
+    print(*a, flush=True)
+
+
+def run(c, opt, **kw):
+    """Loss and gradients of one case, with outputs pre-filled so that an element
+    that is not written shows."""
+    h, w = c["hidden"], c["weight"]
+    dh = torch.full(h.shape, float("nan"), dtype=h.dtype, device=h.device)
+    dw = torch.full(w.shape, float("nan"), dtype=w.dtype, device=w.device)
+    if "target" in c:
+        loss, saved = losses.linear_xent(h, w, c["target"], **opt)
+        losses.linear_xent_grad(h, w, c["target"], saved, c["up"], dhidden=dh, dweight=dw, **opt,
+                                **kw)
+    else:
+        loss, saved = losses.linear_distill(h, w, c["index"], c["logit"], **opt)
+        losses.linear_distill_grad(h, w, c["index"], c["logit"], saved, c["up"], dhidden=dh,
+                                   dweight=dw, **opt, **kw)
+    return loss, saved, dh, dw
+
+
+def ref_opt(opt):
+    r = dict(opt)
+    if "label_smoothing" in r:
+        r["smoothing"] = r.pop("label_smoothing")
+    return r
+
+
+def verify(c, opt, **kw):
+    loss, saved, dh, dw = run(c, opt, **kw)
+    torch.cuda.synchronize()
+    r_loss, r_lse, r_dh, r_dw, b = reference(c, **ref_opt(opt))
+    worst = [check("loss", loss, r_loss, b["loss"]), check("lse", saved.lse, r_lse, b["lse"]),
+             check("dhidden", dh, r_dh, b["dh"]), check("dweight", dw, r_dw, b["dw"])]
+    say("  share of the bounds:", " ".join(f"{x:.2g}" for x in worst))
+    return loss, saved, dh, dw
+
+
+SHAPES = [(1, 1, 1), (1, 2, 3), (2, 33, 64), (3, 70, 8), (17, 300, 65), (64, 257, 96),
+          (65, 64, 128), (130, 1000, 72), (257, 515, 320), (5, 4099, 40), (300, 129, 1),
+          (31, 2049, 640)]
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_xent(shape, dtype):
+    say(f"[case] xent {shape} {dtype}")
+    verify(make(*shape, dtype, seed=sum(shape)), {})
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("shape,k", [((1, 1, 1), 1), ((2, 33, 64), 5), ((17, 300, 65), 16),
+                                     ((64, 257, 96), 17), ((130, 1000, 72), 64),
+                                     ((257, 515, 320), 100), ((9, 40, 24), 1024)], ids=str)
+def test_distill(shape, k, dtype):
+    say(f"[case] distill {shape} k={k} {dtype}")
+    for tau in (1.0, 2.5):
+        verify(make(*shape, dtype, seed=sum(shape) + k, k=k), {"temperature": tau})
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("opt", [{"label_smoothing": 0.1}, {"z_loss": 1e-3},
+                                 {"label_smoothing": 0.3, "z_loss": 1e-2}], ids=str)
+def test_xent_options(opt, dtype):
+    say(f"[case] xent {opt} {dtype}")
+    verify(make(100, 777, 136, dtype, seed=3), opt)
+
+
+@pytest.mark.parametrize("op", ["xent", "distill"])
+@pytest.mark.parametrize("dtype,T,V", [("fp32", 16385, 6001), ("bf16", 70000, 4500)])
+def test_several_pieces(op, dtype, T, V):
+    """More tokens than one piece of the whole vocabulary holds."""
+    say(f"[case] {op} pieces {T} x {V} {dtype}")
+    c = make(T, V, 64, dtype, seed=5, k=0 if op == "xent" else 7)
+    c["up"] = c["up"] * 100
+    verify(c, {} if op == "xent" else {"temperature": 2.0})
+
+
+@pytest.mark.parametrize("op", ["xent", "distill"])
+@pytest.mark.parametrize("dtype", list(DTYPES))
+def test_wide_rows_and_few_tokens(op, dtype):
+    """The vocabulary sum of dhidden split into runs."""
+    say(f"[case] {op} split {dtype}")
+    verify(make(3, 20011, 192, dtype, seed=6, k=0 if op == "xent" else 9), {})
+
+
+@pytest.mark.parametrize("op", ["xent", "distill"])
+@pytest.mark.parametrize("dtype", list(DTYPES))
+def test_empty_rows_may_hold_anything(op, dtype):
+    say(f"[case] {op} garbage in empty rows {dtype}")
+    c = make(77, 200, 64, dtype, seed=7, ignored=0.5, k=0 if op == "xent" else 4)
+    dead = c["target"] == -100 if op == "xent" else (c["index"] < 0).all(1)
+    assert dead.any() and not dead.all()
+    at = torch.nonzero(dead)[:, 0]
+    c["hidden"][at] = float("nan")
+    c["hidden"][at[::2]] = float("inf")
+    c["up"][at] = float("nan")
+    if op == "distill":
+        c["logit"][at] = float("nan")
+    _, saved, dh, _ = verify(c, {})
+    assert (dh[at] == 0).all() and (saved.lse[at] == 0).all()
+
+
+@pytest.mark.parametrize("op", ["xent", "distill"])
+def test_no_live_row(op):
+    say(f"[case] {op} no live row")
+    c = make(40, 300, 64, "bf16", seed=8, ignored=2.0, k=0 if op == "xent" else 3)
+    c["hidden"].fill_(float("nan"))
+    loss, saved, dh, dw = run(c, {})
+    assert (loss == 0).all() and (dh == 0).all() and (dw == 0).all() and (saved.lse == 0).all()
+
+
+@pytest.mark.parametrize("op", ["xent", "distill"])
+def test_no_tokens(op):
+    say(f"[case] {op} no tokens")
+    c = make(0, 300, 64, "bf16", seed=8, k=0 if op == "xent" else 3)
+    loss, saved, dh, dw = run(c, {})
+    assert loss.numel() == 0 and dh.shape == (0, 64) and (dw == 0).all()
+
+
+@pytest.mark.parametrize("wide", [torch.int32, torch.int64])
+def test_bad_targets_give_nan_and_no_gradient(wide):
+    say(f"[case] bad targets {wide}")
+    c = make(50, 200, 64, "bf16", seed=9)
+    c["target"] = c["target"].to(wide)
+    c["target"][3], c["target"][10], c["target"][20] = 200, -1, 2 ** 31 - 1
+    loss, _, dh, _ = verify(c, {})
+    assert torch.isnan(loss[[3, 10, 20]]).all() and (dh[[3, 10, 20]] == 0).all()
+    c = make(50, 200, 64, "fp32", seed=9, k=5)
+    c["index"] = c["index"].to(wide)
+    c["index"][4, 2], c["index"][5, 0] = 200, 2 ** 31 - 1
+    loss, _, dh, _ = verify(c, {"temperature": 2.0})
+    assert torch.isnan(loss[[4, 5]]).all() and (dh[[4, 5]] == 0).all()
+
+
+def test_ignore_index_inside_the_vocabulary():
+    say("[case] ignore_index 0")
+    c = make(50, 20, 64, "bf16", seed=10)
+    c["target"][c["target"] == -100] = 0
+    verify(c, {"ignore_index": 0})
+
+
+def test_teacher_logits_of_minus_infinity_are_padding():
+    say("[case] teacher -inf")
+    c = make(30, 100, 64, "fp32", seed=11, k=6)
+    c["logit"][:, 3] = -math.inf
+    c["logit"][5] = -math.inf
+    _, _, dh, _ = verify(c, {"temperature": 2.0})
+    assert (dh[5] == 0).all()
+
+
+@pytest.mark.parametrize("teacher", list(DTYPES))
+def test_teacher_types_and_strides(teacher):
+    say(f"[case] teacher {teacher}")
+    c = make(33, 100, 64, "bf16", seed=12, k=11)
+    wide = torch.zeros(33, 20, dtype=DTYPES[teacher], device="cuda")
+    wide[:, 4:15] = c["logit"].to(DTYPES[teacher])
+    c["logit"] = wide[:, 4:15]
+    idx = torch.zeros(33, 13, dtype=torch.int32, device="cuda")
+    idx[:, 1:12] = c["index"].int()
+    c["index"] = idx[:, 1:12]
+    verify(c, {"temperature": 2.0})
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("off", [0, 1, 4])
+def test_strided_and_unaligned_tensors(dtype, off):
+    """hidden a slice of wider rows, weight and dweight views of flat buffers at
+    any element offset, dhidden beside hidden in one buffer."""
+    say(f"[case] views {dtype} offset {off}")
+    T, V, D = 70, 150, 128
+    c = make(T, V, D, dtype, seed=13)
+    dt = DTYPES[dtype]
+    flat = torch.zeros(V * D + 64, dtype=dt, device="cuda")
+    flat[off:off + V * D] = c["weight"].reshape(-1)
+    c["weight"] = flat[off:off + V * D].view(V, D)
+    both = torch.full((T, 2 * D + 24), float("nan"), dtype=dt, device="cuda")
+    both[:, off:off + D] = c["hidden"]
+    c["hidden"] = both[:, off:off + D]
+    gflat = torch.full((V * D + 64,), 7.0, dtype=dt, device="cuda")
+    dw = gflat[off:off + V * D].view(V, D)
+    dh = both[:, off + D + 8:off + 2 * D + 8]
+    loss, saved = losses.linear_xent(c["hidden"], c["weight"], c["target"])
+    losses.linear_xent_grad(c["hidden"], c["weight"], c["target"], saved, c["up"], dhidden=dh,
+                            dweight=dw)
+    r_loss, _, r_dh, r_dw, b = reference(c)
+    check("loss", loss, r_loss, b["loss"])
+    check("dhidden", dh, r_dh, b["dh"])
+    check("dweight", dw, r_dw, b["dw"])
+    assert (gflat[:off] == 7).all() and (gflat[off + V * D:] == 7).all()
+    assert torch.isnan(both[:, off + D:off + D + 8]).all()
+
+
+@pytest.mark.parametrize("op", ["xent", "distill"])
+def test_one_gradient_alone_and_broadcast_upstream(op):
+    say(f"[case] {op} one gradient")
+    c = make(70, 150, 128, "bf16", seed=14, k=0 if op == "xent" else 5)
+    c["up"] = torch.full((1,), 0.01, device="cuda").expand(70)
+    _, saved, dh, dw = verify(c, {})
+    fn, t = ((losses.linear_xent_grad, (c["target"],)) if op == "xent" else
+             (losses.linear_distill_grad, (c["index"], c["logit"])))
+    a, none = fn(c["hidden"], c["weight"], *t, saved, 0.01, need_dweight=False)
+    assert none is None and torch.equal(a, dh)
+    none, b = fn(c["hidden"], c["weight"], *t, saved, c["up"][:1], need_dhidden=False)
+    assert none is None and torch.equal(b, dw)
+
+
+@pytest.mark.parametrize("op", ["xent", "distill"])
+def test_the_same_call_gives_the_same_bits_on_any_stream(op):
+    say(f"[case] {op} repeat, streams")
+    c = make(200, 3000, 256, "bf16", seed=15, k=0 if op == "xent" else 8)
+    one = run(c, {})
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        two = run(c, {})
+    s.synchronize()
+    for x, y in zip((one[0], one[1].lse, *one[2:]), (two[0], two[1].lse, *two[2:])):
+        assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("op", ["xent", "distill"])
+def test_captured_into_a_graph(op):
+    say(f"[case] {op} graph")
+    a = make(90, 500, 128, "bf16", seed=16, k=0 if op == "xent" else 8)
+    b = make(90, 500, 128, "bf16", seed=17, ignored=0.6, k=0 if op == "xent" else 8)
+    want = [run(a, {}), run(b, {})]
+    static = {k: v.clone() for k, v in a.items()}
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        run(static, {})
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run(static, {})
+    for i in (0, 1, 0, 1, 1):
+        for k, v in (a, b)[i].items():
+            static[k].copy_(v)
+        graph.replay()
+        torch.cuda.synchronize()
+        run((a, b)[1 - i], {})  # the program's own eager work in between
+        for x, y in zip((out[0], out[1].lse, *out[2:]),
+                        (want[i][0], want[i][1].lse, *want[i][2:])):
+            assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("op", ["xent", "distill"])
+def test_gradient_against_differences(op):
+    """Central differences of the loss along each row's gradient, tilted by a
+    random direction. With step s the loss's own error (its bound, summed over
+    rows) enters as that over s, and the third derivative, at most 2 |dz|^3 a row
+    for a softmax (|dz| the largest change of a logit per unit step), as s^2 / 6."""
+    say(f"[case] {op} differences")
+    c = make(24, 90, 48, "fp32", seed=18, k=0 if op == "xent" else 6)
+    c["up"] = torch.full((24,), 0.1, device="cuda")
+    opt = {"z_loss": 1e-3, "label_smoothing": 0.1} if op == "xent" else {"temperature": 1.5}
+    _, _, dh, dw = run(c, opt)
+    up = c["up"].double()
+    g = torch.Generator().manual_seed(19)
+    tau = opt.get("temperature", 1.0)
+    s = 2.0 ** -6
+    for which, grad in (("hidden", dh), ("weight", dw)):
+        tilt = torch.randn(c[which].shape, generator=g).cuda()
+        d = grad / grad.norm(dim=1, keepdim=True).clamp(min=1e-20) \
+            + 0.3 * tilt / tilt.norm(dim=1, keepdim=True)
+        ends = []
+        for sign in (1, -1):
+            m = dict(c)
+            m[which] = c[which] + sign * s * d
+            ends.append(float((up * run(m, opt)[0].double()).sum()))
+        slope = (ends[0] - ends[1]) / (2 * s)
+        noise = float((up * reference(c, **ref_opt(opt))[4]["loss"]).sum()) * 2 / s
+        if which == "hidden":
+            dz = (d.double() @ c["weight"].double().T).abs().amax(1) / tau
+        else:
+            dz = (c["hidden"].double() @ d.double().T).abs().amax(1) / tau
+        live = (c["target"] != -100) if op == "xent" else (c["index"] >= 0).any(1)
+        curve = s * s / 6 * float((up * live * 2 * tau * tau * dz ** 3).sum()) * 1.1
+        # the moved inputs are rounded: 2^-24 of their size, felt over a step of 2 s
+        moved = float((grad.double().abs() * c[which].double().abs()).sum()) * 2.0 ** -24 / s
+        got = float((grad.double() * d.double()).sum())
+        tol = noise + curve + moved
+        say(f"  {which}: {got:.6g} against {slope:.6g}, tolerance {tol:.2g}")
+        assert tol < 0.2 * abs(got)
+        assert abs(got - slope) <= tol
+
+
+def test_extreme_logits():
+    """Probabilities of one and zero, and logits around +-200."""
+    say("[case] extreme logits")
+    for dtype in DTYPES:
+        c = make(40, 300, 64, dtype, seed=20, spread=60.0)
+        verify(c, {})
+
+
+def test_gradients_land_in_a_worker_buffer_and_step():
+    """Both losses as one model's step: each logical worker's head gradient is
+    written straight into its flat gradient buffer, and the sharded step's
+    averaged gradient is the mean of what the formula gives."""
+    from zero_sharded_optimizer_amd.optimizer import ZeroOptimizer
+    say("[case] losses into the sharded step")
+    g = torch.Generator().manual_seed(21)
+    body = torch.nn.Linear(24, 64, bias=False)
+    head = torch.nn.Parameter(torch.randn(301, 64, generator=g) * 0.1)
+    with torch.no_grad():
+        body.weight.copy_(torch.randn(64, 24, generator=g) * 0.2)
+    body, head = body.cuda(), torch.nn.Parameter(head.detach().cuda())
+    zo = ZeroOptimizer([body.weight, head], 2, 1, precision="fp32", lr=1e-2)
+    zo.zero_grad()
+    total = torch.zeros(301, 64, dtype=torch.float64, device="cuda")
+    for k in range(2):
+        x = torch.randn(30, 24, generator=g).cuda()
+        h = body(x)
+        c = make(30, 301, 64, "fp32", seed=22 + k, k=0 if k == 0 else 4)
+        c["hidden"], c["weight"] = h.detach(), head.detach()
+        c["up"] = torch.full((30,), 1 / 30, device="cuda")
+        gb, gh = zo.worker_grads(k)
+        if k == 0:
+            _, saved = losses.linear_xent(h.detach(), head.detach(), c["target"])
+            dh, _ = losses.linear_xent_grad(h.detach(), head.detach(), c["target"], saved, 1 / 30,
+                                            dweight=gh)
+        else:
+            _, saved = losses.linear_distill(h.detach(), head.detach(), c["index"], c["logit"])
+            dh, _ = losses.linear_distill_grad(h.detach(), head.detach(), c["index"], c["logit"],
+                                               saved, 1 / 30, dweight=gh)
+        body.weight.grad = None
+        h.backward(dh)
+        gb.copy_(body.weight.grad)
+        _, _, _, dw, b = reference(c)
+        check("head gradient", gh, dw, b["dw"])
+        total += gh.double()
+    before = head.detach().clone()
+    zo.step()
+    mean = zo.averaged_grad()[body.weight.numel():].view(301, 64).double()
+    assert float((mean - total / 2).abs().max()) <= 2.0 ** -22 * float(total.abs().max())
+    assert not torch.equal(before, head.detach())

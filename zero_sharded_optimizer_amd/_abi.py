@@ -1,4 +1,4 @@
-"""ctypes declarations of the C ABI in include/zero_adam.h.
+"""ctypes declarations of the C ABI in include/zero_adam.h and include/zero_loss.h.
 
 Loading the library touches no GPU: libzero.so makes no HIP call until a
 function that enqueues device work is called with valid arguments.
@@ -23,6 +23,13 @@ ZERO_OPT_ADAM = 0
 ZERO_OPT_SGD = 1
 
 ZERO_MAX_WORKERS = 256
+
+ZERO_LOSS_F32 = 0
+ZERO_LOSS_BF16 = 1
+ZERO_LOSS_F16 = 2
+ZERO_INDEX_I32 = 0
+ZERO_INDEX_I64 = 1
+ZERO_LOSS_MAX_K = 1024
 
 STATUS_NAMES = {ZERO_OK: "ZERO_OK", ZERO_EINVAL: "ZERO_EINVAL",
                 ZERO_EUNSUPPORTED: "ZERO_EUNSUPPORTED", ZERO_EHIP: "ZERO_EHIP"}
@@ -61,11 +68,38 @@ class zero_mem(C.Structure):
                 ("total", C.c_int64)]
 
 
+class zero_head(C.Structure):
+    _fields_ = [("tokens", C.c_int64), ("vocab", C.c_int64), ("dim", C.c_int64),
+                ("hidden", C.c_void_p), ("hidden_stride", C.c_int64),
+                ("weight", C.c_void_p), ("weight_stride", C.c_int64),
+                ("dtype", C.c_int32), ("reserved", C.c_int32)]
+
+
+class zero_xent_params(C.Structure):
+    _fields_ = [("target", C.c_void_p), ("index_dtype", C.c_int32), ("reserved", C.c_int32),
+                ("ignore_index", C.c_int64), ("label_smoothing", C.c_double),
+                ("z_loss", C.c_double)]
+
+
+class zero_distill_params(C.Structure):
+    _fields_ = [("index", C.c_void_p), ("logit", C.c_void_p), ("index_stride", C.c_int64),
+                ("logit_stride", C.c_int64), ("k", C.c_int32), ("index_dtype", C.c_int32),
+                ("logit_dtype", C.c_int32), ("reserved", C.c_int32), ("temperature", C.c_double)]
+
+
+class zero_head_grads(C.Structure):
+    _fields_ = [("upstream", C.c_void_p), ("upstream_stride", C.c_int64),
+                ("dhidden", C.c_void_p), ("dhidden_stride", C.c_int64),
+                ("dweight", C.c_void_p), ("dweight_stride", C.c_int64)]
+
+
 EXPORTED = ("zero_init_states", "zero_step", "zero_memory_bytes", "zero_shard_bounds",
             "zero_last_error", "zero_mean_grad_workspace_bytes", "zero_mean_grad",
             "zero_step_mean", "zero_step_clipped_workspace_bytes", "zero_step_clipped",
             "zero_step_range", "zero_step_scalars_fill", "zero_step_range_dev", "zero_min_stage",
-            "zero_step_buckets", "zero_step_with_mean", "zero_mean_grad_noalloc")
+            "zero_step_buckets", "zero_step_with_mean", "zero_mean_grad_noalloc",
+            "zero_loss_workspace_bytes", "zero_linear_xent", "zero_linear_xent_grad",
+            "zero_linear_distill", "zero_linear_distill_grad")
 
 _lib = None
 
@@ -149,6 +183,24 @@ def load(path=None):
     lib.zero_min_stage.argtypes = [C.c_int64, C.c_int32, C.c_int32, C.c_int64, C.c_int64,
                                     C.POINTER(C.c_int32)]
     lib.zero_min_stage.restype = C.c_int
+    lib.zero_loss_workspace_bytes.argtypes = [C.POINTER(zero_head), C.c_int32,
+                                              C.POINTER(C.c_size_t)]
+    lib.zero_loss_workspace_bytes.restype = C.c_int
+    lib.zero_linear_xent.argtypes = [C.POINTER(zero_head), C.POINTER(zero_xent_params), C.c_void_p,
+                                     C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]
+    lib.zero_linear_xent.restype = C.c_int
+    lib.zero_linear_xent_grad.argtypes = [C.POINTER(zero_head), C.POINTER(zero_xent_params),
+                                          C.c_void_p, C.POINTER(zero_head_grads), C.c_void_p,
+                                          C.c_size_t, C.c_void_p]
+    lib.zero_linear_xent_grad.restype = C.c_int
+    lib.zero_linear_distill.argtypes = [C.POINTER(zero_head), C.POINTER(zero_distill_params),
+                                        C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p,
+                                        C.c_size_t, C.c_void_p]
+    lib.zero_linear_distill.restype = C.c_int
+    lib.zero_linear_distill_grad.argtypes = [C.POINTER(zero_head), C.POINTER(zero_distill_params),
+                                             C.c_void_p, C.c_void_p, C.POINTER(zero_head_grads),
+                                             C.c_void_p, C.c_size_t, C.c_void_p]
+    lib.zero_linear_distill_grad.restype = C.c_int
     lib.zero_last_error.argtypes = []
     lib.zero_last_error.restype = C.c_char_p
     if path is None:

@@ -2,9 +2,9 @@
 libzceil.so, the streaming-ceiling kernels that bench.py measures the memory
 system with.
 
-The host layer (zero_abi.cpp) is compiled with g++; the kernels
-(zero_kernels.hip) and the stream helpers (zero_runtime.hip) with hipcc for
-gfx950. Both with multiply-add contraction
+The host layers (zero_abi.cpp, zero_loss_abi.cpp) are compiled with g++; the
+kernels (zero_kernels.hip for the step, zero_loss.hip for the loss operators)
+and the stream helpers (zero_runtime.hip) with hipcc for gfx950. Both with multiply-add contraction
 off and IEEE division / square root, because the step's result is defined
 operation by operation. Packed fp32 instructions are disabled for the device
 code.
@@ -40,17 +40,21 @@ def _run(cmd):
 
 
 def build(verbose=False):
-    """Compile both translation units and link libzero.so next to this file."""
+    """Compile every translation unit and link libzero.so next to this file."""
     os.makedirs(BUILD, exist_ok=True)
     abi_o = os.path.join(BUILD, "zero_abi.o")
     ker_o = os.path.join(BUILD, "zero_kernels.o")
     rt_o = os.path.join(BUILD, "zero_runtime.o")
+    loss_abi_o = os.path.join(BUILD, "zero_loss_abi.o")
+    loss_o = os.path.join(BUILD, "zero_loss.o")
     steps = [
         ["g++", *HOST_FLAGS, "-c", os.path.join(CSRC, "zero_abi.cpp"), "-o", abi_o],
         [HIPCC, *HIP_FLAGS, "-c", os.path.join(CSRC, "zero_kernels.hip"), "-o", ker_o],
         [HIPCC, *HIP_FLAGS, "-c", os.path.join(CSRC, "zero_runtime.hip"), "-o", rt_o],
-        [HIPCC, "-shared", "-fPIC", f"--offload-arch={ARCH}", abi_o, ker_o, rt_o, "-o",
-         LIB + ".tmp"],
+        ["g++", *HOST_FLAGS, "-c", os.path.join(CSRC, "zero_loss_abi.cpp"), "-o", loss_abi_o],
+        [HIPCC, *HIP_FLAGS, "-c", os.path.join(CSRC, "zero_loss.hip"), "-o", loss_o],
+        [HIPCC, "-shared", "-fPIC", f"--offload-arch={ARCH}", abi_o, ker_o, rt_o, loss_abi_o,
+         loss_o, "-o", LIB + ".tmp"],
     ]
     for cmd in steps:
         if verbose:

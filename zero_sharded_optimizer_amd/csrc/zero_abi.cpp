@@ -14,6 +14,7 @@
 #include <utility>
 #include <vector>
 
+#include "zero_error.h"
 #include "zero_launch.h"
 
 static_assert(sizeof(zero_step_scalars) == sizeof(zlaunch::DynScalars) &&
@@ -25,11 +26,10 @@ namespace {
 
 thread_local std::string g_last_error;
 
-// Largest accepted n: 2^56 elements, so that every byte count and address
-// range formed from n (at most 32 bytes per element) stays inside int64_t.
-constexpr int64_t kMaxN = INT64_C(1) << 56;
+}  // namespace
 
-zero_status fail(zero_status st, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+namespace zerror {
+
 zero_status fail(zero_status st, const char* fmt, ...) {
   char buf[512];
   va_list ap;
@@ -44,6 +44,17 @@ zero_status ok() {
   g_last_error.clear();
   return ZERO_OK;
 }
+
+}  // namespace zerror
+
+namespace {
+
+using zerror::fail;
+using zerror::ok;
+
+// Largest accepted n: 2^56 elements, so that every byte count and address
+// range formed from n (at most 32 bytes per element) stays inside int64_t.
+constexpr int64_t kMaxN = INT64_C(1) << 56;
 
 // Shard r of np.array_split(np.arange(n), N) ("ZeRO-Sharded Adam Step",
 // section "The shards"): q = n / N, rho = n % N; the first rho shards have

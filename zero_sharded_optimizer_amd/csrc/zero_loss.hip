@@ -1,0 +1,932 @@
+// gfx950 kernels of the loss operators of include/zero_loss.h: softmax cross
+// entropy and top-K distillation over a vocabulary head, with the gradient.
+//
+// The order of one call:
+//   scan      finds the rows that take part and numbers them (live positions)
+//   pack      copies the live rows of hidden, padded and aligned; rows that
+//             take no part are never read, so what they hold does not matter
+//   logits    [live, piece] = hidden W^T in tiles; the forward reduces each
+//             tile to softmax partials, the gradient turns it into g
+//   dhidden   += g W,   dweight = g^T hidden    (gradient, per piece)
+// Every product is one tiled kernel over 16-bit operands with fp32 sums. fp32
+// inputs go through it as three bf16 parts each (x = hi + mid + lo, exact to
+// 2^-26) and six of the nine part products, small ones first.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "zero_loss_launch.h"
+
+namespace zloss {
+namespace {
+
+typedef uint16_t u16;
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// What the scan leaves for the kernels after it.
+struct Head {
+  int live;         // rows that take part
+  float scale;      // power of two that g is held at
+  float inv_scale;
+};
+
+// Per live row, for the logits' gradient g = a exp(z - lse) - c - hit [j = target].
+struct RowParam {
+  float lse, a, c, hit;
+  int target;       // global vocabulary index, or -1
+  int pad[3];
+};
+static_assert(sizeof(RowParam) == 32, "the plan counts 32 bytes a row");
+
+// The part products of fp32 operands: (left part, right part), small ones first.
+constexpr int kSegs = 6;
+__device__ __constant__ const int kSegA[kSegs] = {1, 2, 0, 1, 0, 0};
+__device__ __constant__ const int kSegB[kSegs] = {1, 0, 2, 0, 1, 0};
+
+// ---- Values ---------------------------------------------------------------
+__device__ __forceinline__ u16 bf16_bits(float x) { return __builtin_bit_cast(u16, (__bf16)x); }
+__device__ __forceinline__ u16 f16_bits(float x) { return __builtin_bit_cast(u16, (_Float16)x); }
+__device__ __forceinline__ float bf16_float(u16 b) {
+  return __builtin_bit_cast(float, (uint32_t)b << 16);
+}
+__device__ __forceinline__ float f16_float(u16 b) {
+  return (float)__builtin_bit_cast(_Float16, b);
+}
+
+// x = p[0] + p[1] + p[2] in bf16 parts. An infinity or NaN is its first part
+// alone (the remainder would be NaN).
+__device__ __forceinline__ void split3(float x, u16 p[3]) {
+  p[0] = bf16_bits(x);
+  const float hi = bf16_float(p[0]);
+  const bool fine = __builtin_isfinite(hi);
+  const float r = fine ? x - hi : 0.0f;
+  p[1] = bf16_bits(r);
+  p[2] = bf16_bits(r - bf16_float(p[1]));
+}
+
+template <int DT>
+__device__ __forceinline__ float load_value(const void* p, int64_t i) {
+  if constexpr (DT == kF32) return static_cast<const float*>(p)[i];
+  const u16 b = static_cast<const u16*>(p)[i];
+  return DT == kBF16 ? bf16_float(b) : f16_float(b);
+}
+
+__device__ __forceinline__ float load_any(const void* p, int64_t i, int dtype) {
+  return dtype == kF32 ? load_value<kF32>(p, i)
+                       : dtype == kBF16 ? load_value<kBF16>(p, i) : load_value<kF16>(p, i);
+}
+
+__device__ __forceinline__ int64_t load_index(const void* p, int64_t i, int wide) {
+  return wide ? static_cast<const int64_t*>(p)[i] : (int64_t) static_cast<const int32_t*>(p)[i];
+}
+
+template <int DT>
+__device__ __forceinline__ void store_value(void* p, int64_t i, float x) {
+  if constexpr (DT == kF32) static_cast<float*>(p)[i] = x;
+  else static_cast<u16*>(p)[i] = DT == kBF16 ? bf16_bits(x) : f16_bits(x);
+}
+
+// Four values to four consecutive elements; `wide`: the address suits one store.
+template <int DT>
+__device__ __forceinline__ void store4(void* p, int64_t i, f32x4 x, bool wide) {
+  if (wide) {
+    if constexpr (DT == kF32) {
+      *reinterpret_cast<f32x4*>(static_cast<float*>(p) + i) = x;
+    } else {
+      u16 b[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) b[r] = DT == kBF16 ? bf16_bits(x[r]) : f16_bits(x[r]);
+      *reinterpret_cast<u32x2*>(static_cast<u16*>(p) + i) =
+          u32x2{b[0] | (uint32_t)b[1] << 16, b[2] | (uint32_t)b[3] << 16};
+    }
+  } else {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) store_value<DT>(p, i + r, x[r]);
+  }
+}
+
+// exp of x in fp32: the product with log2(e) is rounded once, the rest is the
+// hardware's exp2 (1 ulp).
+__device__ __forceinline__ float exp_f(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
+
+template <int DT>
+__device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
+  if constexpr (DT == kF16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
+                                                  __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+__device__ __forceinline__ float wave_max(float x) {
+#pragma unroll
+  for (int d = 32; d; d >>= 1) x = fmaxf(x, __shfl_xor(x, d));
+  return x;
+}
+__device__ __forceinline__ float wave_sum(float x) {
+#pragma unroll
+  for (int d = 32; d; d >>= 1) x += __shfl_xor(x, d);
+  return x;
+}
+
+__device__ __forceinline__ int round_up_int(int x, int m) { return (x + m - 1) / m * m; }
+
+// ---- Rows: which take part ------------------------------------------------
+// Distillation: one wave a row. 1 live, 0 empty, 2 bad.
+__global__ void __launch_bounds__(256) classify_kernel(Call c, uint8_t* state) {
+  const int64_t t = (int64_t)blockIdx.x * 4 + threadIdx.x / 64;
+  if (t >= c.plan.tokens) return;
+  const int lane = threadIdx.x % 64;
+  bool any = false, bad = false;
+  for (int k = lane; k < c.k; k += 64) {
+    const int64_t i = load_index(c.target, t * c.index_stride + k, c.index64);
+    if (i >= c.plan.vocab) bad = true;
+    if (i >= 0) any |= load_any(c.teacher, t * c.logit_stride + k, c.teacher_dtype) != -INFINITY;
+  }
+  any = __any(any);
+  bad = __any(bad);
+  if (lane == 0) state[t] = bad ? 2 : any ? 1 : 0;
+}
+
+// One block numbers the live rows in order, and for the gradient finds the
+// power of two that brings the largest |g| a row can have to [2^14, 2^15):
+// inside fp16's range with 29 bits below it that are not subnormal.
+__global__ void __launch_bounds__(1024) scan_kernel(Call c) {
+  Head* head = reinterpret_cast<Head*>(c.ws + c.plan.o_head);
+  int* rowmap = reinterpret_cast<int*>(c.ws + c.plan.o_rowmap);
+  int* pos = reinterpret_cast<int*>(c.ws + c.plan.o_pos);
+  const uint8_t* state = reinterpret_cast<const uint8_t*>(c.ws + c.plan.o_state);
+  __shared__ int counts[16];
+  __shared__ float tops[16];
+  const int tid = threadIdx.x, wave = tid / 64, lane = tid % 64;
+  int base = 0;
+  float top = 0.0f;
+  for (int64_t t0 = 0; t0 < c.plan.tokens; t0 += 1024) {
+    const int64_t t = t0 + tid;
+    int st = 0;
+    if (t < c.plan.tokens) {
+      if (c.k == 0) {
+        const int64_t y = load_index(c.target, t, c.index64);
+        st = y == c.ignore_index ? 0 : (y >= 0 && y < c.plan.vocab) ? 1 : 2;
+      } else {
+        st = state[t];
+      }
+    }
+    const uint64_t votes = __ballot(st == 1);
+    if (lane == 0) counts[wave] = __popcll(votes);
+    __syncthreads();
+    int before = base, total = 0;
+    for (int w = 0; w < 16; ++w) {
+      if (w < wave) before += counts[w];
+      total += counts[w];
+    }
+    __syncthreads();
+    if (t < c.plan.tokens) {
+      if (st == 1) {
+        const int at = before + __popcll(votes & ((1ull << lane) - 1));
+        rowmap[at] = (int)t;
+        pos[t] = at;
+        if (c.plan.grad) {
+          float u = fabsf(c.upstream[t * c.upstream_stride]) * c.temperature;
+          if (c.z_loss != 0.0f) u *= 1.0f + 2.0f * c.z_loss * fabsf(c.lse_in[t]);
+          top = fmaxf(top, u);
+        }
+      } else {
+        pos[t] = st == 0 ? -1 : -2;
+      }
+    }
+    base += total;
+  }
+  top = wave_max(top);
+  if (lane == 0) tops[wave] = top;
+  __syncthreads();
+  if (tid == 0) {
+    for (int w = 0; w < 16; ++w) top = fmaxf(top, tops[w]);
+    int e = 0;
+    if (top > 0.0f && top < INFINITY) {
+      e = 14 - ilogbf(top);
+      e = e < -100 ? -100 : e > 100 ? 100 : e;
+    }
+    head->live = base;
+    head->scale = ldexpf(1.0f, e);
+    head->inv_scale = ldexpf(1.0f, -e);
+  }
+}
+
+// ---- Packing --------------------------------------------------------------
+// Eight elements from column k of a row, zero beyond `dim`, as 16-bit parts.
+template <int DT>
+__device__ __forceinline__ void pack8(const void* src, int64_t at, int k, int dim, bool wide,
+                                      u32x4 out[3]) {
+  if constexpr (DT != kF32) {
+    if (wide && k + 8 <= dim) {
+      out[0] = *reinterpret_cast<const u32x4*>(static_cast<const u16*>(src) + at + k);
+      return;
+    }
+    u16 b[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) b[i] = k + i < dim ? static_cast<const u16*>(src)[at + k + i] : 0;
+    out[0] = *reinterpret_cast<const u32x4*>(b);
+  } else {
+    u16 parts[3][8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      u16 p[3];
+      split3(k + i < dim ? static_cast<const float*>(src)[at + k + i] : 0.0f, p);
+#pragma unroll
+      for (int s = 0; s < 3; ++s) parts[s][i] = p[s];
+    }
+#pragma unroll
+    for (int s = 0; s < 3; ++s) out[s] = *reinterpret_cast<const u32x4*>(parts[s]);
+  }
+}
+
+// The live rows of hidden, zero rows up to the next multiple of kRowPad.
+template <int DT>
+__global__ void __launch_bounds__(256) pack_hidden_kernel(Call c, bool wide) {
+  const Plan& p = c.plan;
+  const int live = reinterpret_cast<const Head*>(c.ws + p.o_head)->live;
+  const int r = blockIdx.x;
+  if (r >= round_up_int(live, (int)kRowPad)) return;
+  u16* dst = reinterpret_cast<u16*>(c.ws + p.o_h) + (int64_t)r * p.dimp;
+  const bool real = r < live;
+  const int64_t at =
+      real ? reinterpret_cast<const int*>(c.ws + p.o_rowmap)[r] * c.hidden_stride : 0;
+  for (int k = threadIdx.x * 8; k < p.dimp; k += 256 * 8) {
+    u32x4 v[3] = {};
+    if (real) pack8<DT>(c.hidden, at, k, (int)p.dim, wide, v);
+    for (int s = 0; s < (DT == kF32 ? 3 : 1); ++s)
+      *reinterpret_cast<u32x4*>(dst + s * p.rows * p.dimp + k) = v[s];
+  }
+}
+
+// Vocabulary rows [v0, v0 + piece) of the weight, zero rows beyond the last.
+template <int DT>
+__global__ void __launch_bounds__(256) pack_weight_kernel(Call c, int64_t v0, bool wide) {
+  const Plan& p = c.plan;
+  const int64_t r = blockIdx.x;
+  u16* dst = reinterpret_cast<u16*>(c.ws + p.o_w) + r * p.dimp;
+  const bool real = v0 + r < p.vocab;
+  for (int k = threadIdx.x * 8; k < p.dimp; k += 256 * 8) {
+    u32x4 v[3] = {};
+    if (real) pack8<DT>(c.weight, (v0 + r) * c.weight_stride, k, (int)p.dim, wide, v);
+    for (int s = 0; s < (DT == kF32 ? 3 : 1); ++s)
+      *reinterpret_cast<u32x4*>(dst + s * p.piece * p.dimp + k) = v[s];
+  }
+}
+
+// ---- The product ----------------------------------------------------------
+// out[n][m] = sum_k A[m][k] B[n][k]. An operand is stored either with its inner
+// index contiguous (row r, step k at r*ld + k) or with its rows contiguous
+// (k*ld + r, `T` for transposed).
+struct Operand {
+  const u16* p;
+  int64_t plane;   // elements between the parts of fp32 operands
+  int64_t ld;
+  int rows;        // row indices beyond rows - 1 are read as the last (group of 8) there is
+  int steps;       // likewise inner indices, where the other operand holds zeros
+};
+
+struct Product {
+  Operand a, b;
+  int m, n;        // extents (n: the most there can be, where live_n)
+  int inner;       // inner extent, a multiple of 64 (the most there can be, where live_inner)
+  bool live_n, live_inner;  // the extent is the live count, rounded up to 64 for the inner one
+  int segs;        // 1, or kSegs part products
+  int splits;      // the inner extent in this many runs
+  const Head* head;
+};
+
+// 128 x 128 tiles, inner steps of 32, through registers into LDS rows of
+// 32 + 8 elements (the pad spreads the rows over the banks). Four waves, each
+// 64 x 64 of the tile in 4 x 4 matrix instructions 16x16x32.
+template <int DT, bool TA, bool TB, class Epi>
+__global__ void __launch_bounds__(256) product_kernel(Product g, Epi epi) {
+  constexpr int BM = 128, BN = 128, BK = 32, LD = BK + 8;
+  __shared__ __attribute__((aligned(16))) u16 As[BM * LD];
+  __shared__ __attribute__((aligned(16))) u16 Bs[BN * LD];
+  const int live = g.head->live;
+  const int n_ext = g.live_n ? live : g.n;
+  const int inner = g.live_inner ? round_up_int(live, 64) : g.inner;
+  const int m0 = blockIdx.x * BM, n0 = blockIdx.y * BN;
+  if (n0 >= n_ext) return;
+  const int chunk = round_up_int((inner + g.splits - 1) / g.splits, 64);
+  const int k_lo = min(inner, (int)blockIdx.z * chunk), k_hi = min(inner, k_lo + chunk);
+  const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
+  const int wm = (wave & 1) * 64, wn = (wave >> 1) * 64;
+
+  f32x4 acc[4][4] = {};
+  const auto load = [&](const Operand& o, const u16* base, bool t, int r0, int k0, int part) {
+    const int id = tid + part * 256;  // 512 groups of 8 elements a tile
+    if (!t) {
+      const int r = min(r0 + id / 4, o.rows - 1), k = k0 + (id % 4) * 8;
+      return *reinterpret_cast<const u32x4*>(base + (int64_t)r * o.ld + k);
+    }
+    const int k = min(k0 + id / 16, o.steps - 1), r = min(r0 + (id % 16) * 8, o.rows - 8);
+    return *reinterpret_cast<const u32x4*>(base + (int64_t)k * o.ld + r);
+  };
+  const auto keep = [&](u16* s, bool t, int part, u32x4 v) {
+    const int id = tid + part * 256;
+    if (!t) {
+      *reinterpret_cast<u32x4*>(s + (id / 4) * LD + (id % 4) * 8) = v;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        s[((id % 16) * 8 + i) * LD + id / 16] = (u16)(v[i / 2] >> (16 * (i % 2)));
+    }
+  };
+  for (int seg = 0; seg < g.segs; ++seg) {
+    const u16* a = g.a.p + (g.segs > 1 ? kSegA[seg] * g.a.plane : 0);
+    const u16* b = g.b.p + (g.segs > 1 ? kSegB[seg] * g.b.plane : 0);
+    for (int k0 = k_lo; k0 < k_hi; k0 += BK) {
+      u32x4 va[2], vb[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        va[i] = load(g.a, a, TA, m0, k0, i);
+        vb[i] = load(g.b, b, TB, n0, k0, i);
+      }
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        keep(As, TA, i, va[i]);
+        keep(Bs, TB, i, vb[i]);
+      }
+      __syncthreads();
+      u32x4 fa[4], fb[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        fa[i] = *reinterpret_cast<const u32x4*>(As + (wm + i * 16 + lane % 16) * LD +
+                                                lane / 16 * 8);
+        fb[i] = *reinterpret_cast<const u32x4*>(Bs + (wn + i * 16 + lane % 16) * LD +
+                                                lane / 16 * 8);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = mfma<DT>(fa[i], fb[j], acc[i][j]);
+    }
+  }
+  epi.template tile<4, 4>(m0 + wm, n0 + wn, n_ext, (int)blockIdx.z, acc);
+}
+
+// ---- What happens to a tile -------------------------------------------------
+// A wave holds MI x NJ squares of 16 x 16: column n0 + 16 j + lane % 16, rows
+// m0 + 16 i + lane / 16 * 4 + 0..3.
+
+// Forward: the tile's rows m are vocabulary, its columns n live rows. Each wave
+// leaves the largest logit, the sum of exponentials and the sum of logits of
+// its stretch of the vocabulary.
+struct StatEpi {
+  float2* stat;
+  float* sum;       // nullptr where nobody asks for it
+  int64_t cols;     // partials per row
+  float inv_temp;
+  int m_base;       // vocabulary index of m = 0
+  int vocab;
+  template <int MI, int NJ>
+  __device__ __forceinline__ void tile(int m0, int n0, int n_ext, int, f32x4 (&acc)[MI][NJ]) {
+    static_assert(MI * 16 == kStatRows, "one partial per wave");
+    const int lane = threadIdx.x % 64;
+    const int m_hi = vocab - m_base;
+    if (m0 >= round_up_int(m_hi, (int)kStatRows)) return;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      float top = -INFINITY, total = 0.0f, plain = 0.0f;
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const bool in = m0 + i * 16 + lane / 16 * 4 + r < m_hi;
+          const float z = in ? acc[i][j][r] * inv_temp : -INFINITY;
+          acc[i][j][r] = z;
+          plain += in ? z : 0.0f;
+          top = fmaxf(top, z);
+        }
+      top = fmaxf(top, __shfl_xor(top, 16));
+      top = fmaxf(top, __shfl_xor(top, 32));
+      const float from = top == -INFINITY ? 0.0f : top;  // -inf - -inf would be NaN
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) total += exp_f(acc[i][j][r] - from);
+      total += __shfl_xor(total, 16);
+      total += __shfl_xor(total, 32);
+      plain += __shfl_xor(plain, 16);
+      plain += __shfl_xor(plain, 32);
+      const int n = n0 + j * 16 + lane % 16;
+      if (lane < 16 && n < n_ext) {
+        const int64_t at = n * cols + (m_base + m0) / kStatRows;
+        stat[at] = make_float2(top, total);
+        if (sum != nullptr) sum[at] = plain;
+      }
+    }
+  }
+};
+
+// Gradient: the same tile becomes g, [rows][ld] with the vocabulary
+// contiguous. Rows beyond the live ones and columns beyond the vocabulary hold
+// zeros, so that the products over g need not know either.
+template <int DT>
+struct GradEpi {
+  const RowParam* rows;
+  u16* g;
+  int64_t plane, ld;
+  float inv_temp;
+  int m_base, m_ext;   // first vocabulary index, how many of it are real
+  template <int MI, int NJ>
+  __device__ __forceinline__ void tile(int m0, int n0, int n_ext, int, f32x4 (&acc)[MI][NJ]) {
+    const int lane = threadIdx.x % 64;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const int n = n0 + j * 16 + lane % 16;
+      const RowParam rp = rows[n];
+      const bool real = n < n_ext;
+      const int at = rp.target - m_base;
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        const int m = m0 + i * 16 + lane / 16 * 4;
+        u16 parts[3][4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          float x = rp.a * exp_f(acc[i][j][r] * inv_temp - rp.lse) - rp.c;
+          if (m + r == at) x -= rp.hit;
+          x = real && m + r < m_ext ? x : 0.0f;
+          if constexpr (DT == kF32) {
+            u16 p[3];
+            split3(x, p);
+            for (int s = 0; s < 3; ++s) parts[s][r] = p[s];
+          } else {
+            parts[0][r] = DT == kBF16 ? bf16_bits(x) : f16_bits(x);
+          }
+        }
+        if (m < ld) {
+#pragma unroll
+          for (int s = 0; s < (DT == kF32 ? 3 : 1); ++s)
+            *reinterpret_cast<u32x2*>(g + s * plane + n * ld + m) =
+                u32x2{parts[s][0] | (uint32_t)parts[s][1] << 16,
+                      parts[s][2] | (uint32_t)parts[s][3] << 16};
+        }
+      }
+    }
+  }
+};
+
+// dhidden's sum over the vocabulary: fp32 [splits][rows][ld], added to from the
+// second piece on. Rows m are hidden's columns, columns n live rows.
+struct SumEpi {
+  float* acc_out;
+  int64_t slab, ld;
+  int m_ext;
+  bool add;
+  template <int MI, int NJ>
+  __device__ __forceinline__ void tile(int m0, int n0, int n_ext, int split,
+                                       f32x4 (&acc)[MI][NJ]) {
+    const int lane = threadIdx.x % 64;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const int n = n0 + j * 16 + lane % 16;
+      if (n >= n_ext) continue;
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        const int m = m0 + i * 16 + lane / 16 * 4;
+        if (m >= m_ext) continue;
+        f32x4* o = reinterpret_cast<f32x4*>(acc_out + split * slab + n * ld + m);
+        *o = add ? *o + acc[i][j] : acc[i][j];
+      }
+    }
+  }
+};
+
+// dweight: rows m are hidden's columns, columns n the piece's vocabulary.
+template <int DT>
+struct WeightEpi {
+  void* out;
+  int64_t ld;
+  int64_t v0;
+  int m_ext;
+  bool wide;       // rows start at multiples of four elements' size
+  const Head* head;
+  template <int MI, int NJ>
+  __device__ __forceinline__ void tile(int m0, int n0, int n_ext, int, f32x4 (&acc)[MI][NJ]) {
+    const int lane = threadIdx.x % 64;
+    const float s = head->inv_scale;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const int n = n0 + j * 16 + lane % 16;
+      if (n >= n_ext) continue;
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        const int m = m0 + i * 16 + lane / 16 * 4;
+        const f32x4 x = acc[i][j] * s;
+        if (m + 4 <= m_ext) {
+          store4<DT>(out, (v0 + n) * ld + m, x, wide);
+        } else {
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (m + r < m_ext) store_value<DT>(out, (v0 + n) * ld + m + r, x[r]);
+        }
+      }
+    }
+  }
+};
+
+// ---- Rows: the losses -------------------------------------------------------
+// The logits of up to 16 vocabulary rows (one per lane % 16) against one live
+// row, by the same matrix instructions in the same order as the tiles', so that
+// they are the same bits as the ones in the softmax's sum: in a loss near zero
+// the two have to cancel. Lane l gets rows l / 16 * 4 + 0..3.
+template <int DT>
+__device__ __forceinline__ f32x4 gather_logits(const Call& c, int64_t row, int live_row,
+                                               bool wide) {
+  const Plan& p = c.plan;
+  const int lane = threadIdx.x % 64;
+  const u16* h = reinterpret_cast<const u16*>(c.ws + p.o_h) + (int64_t)live_row * p.dimp;
+  const int64_t at = row * c.weight_stride;
+  f32x4 acc = {};
+  for (int seg = 0; seg < (DT == kF32 ? kSegs : 1); ++seg) {
+    const int sa = DT == kF32 ? kSegA[seg] : 0, sb = DT == kF32 ? kSegB[seg] : 0;
+    for (int k = lane / 16 * 8; k < p.dimp; k += 32) {
+      u32x4 a[3];
+      pack8<DT>(c.weight, at, k, (int)p.dim, wide, a);
+      const u32x4 b = *reinterpret_cast<const u32x4*>(h + sb * p.rows * p.dimp + k);
+      acc = mfma<DT>(DT == kF32 ? (sa == 0 ? a[0] : sa == 1 ? a[1] : a[2]) : a[0], b, acc);
+    }
+  }
+  return acc;
+}
+
+template <int N>
+__device__ __forceinline__ float block_max(float x, float* s) {
+  x = wave_max(x);
+  __syncthreads();
+  if (threadIdx.x % 64 == 0) s[threadIdx.x / 64] = x;
+  __syncthreads();
+  for (int w = 0; w < N; ++w) x = fmaxf(x, s[w]);
+  return x;
+}
+template <int N>
+__device__ __forceinline__ float block_sum(float x, float* s) {
+  x = wave_sum(x);
+  __syncthreads();
+  if (threadIdx.x % 64 == 0) s[threadIdx.x / 64] = x;
+  __syncthreads();
+  x = 0.0f;
+  for (int w = 0; w < N; ++w) x += s[w];
+  return x;
+}
+
+// One block a token: joins the partials, gathers the targets' logits, writes
+// the loss.
+template <int DT>
+__global__ void __launch_bounds__(256) loss_kernel(Call c, bool wide) {
+  const Plan& p = c.plan;
+  const int64_t t = blockIdx.x;
+  const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
+  const int K = c.k == 0 ? 1 : c.k;
+  __shared__ float red[4];
+  __shared__ float zs[1024];
+  __shared__ float ls[1024];
+  const int at = reinterpret_cast<const int*>(c.ws + p.o_pos)[t];
+  if (at < 0) {
+    if (tid == 0) {
+      c.loss[t] = at == -2 ? __builtin_nanf("") : 0.0f;
+      c.lse[t] = 0.0f;
+    }
+    if (c.logit != nullptr)
+      for (int k = tid; k < K; k += 256) c.logit[t * K + k] = 0.0f;
+    return;
+  }
+  // largest logit m and sum s of exp(z - m) over the vocabulary
+  const float2* stat = reinterpret_cast<const float2*>(c.ws + p.o_stat) + at * p.stat_cols;
+  const int cols = (int)((p.vocab + kStatRows - 1) / kStatRows);
+  float m = -INFINITY;
+  for (int i = tid; i < cols; i += 256) m = fmaxf(m, stat[i].x);
+  m = block_max<4>(m, red);
+  const float from = m == -INFINITY ? 0.0f : m;
+  float s = 0.0f, plain = 0.0f;
+  for (int i = tid; i < cols; i += 256) s += stat[i].y * exp_f(stat[i].x - from);
+  s = block_sum<4>(s, red);
+  if (c.smoothing != 0.0f) {
+    const float* sum = reinterpret_cast<const float*>(c.ws + p.o_sum) + at * p.stat_cols;
+    for (int i = tid; i < cols; i += 256) plain += sum[i];
+    plain = block_sum<4>(plain, red);
+  }
+  // the targets' logits, 16 a wave
+  for (int k0 = wave * 16; k0 < K; k0 += 64) {
+    const int k = k0 + lane % 16;
+    int64_t row = -1;
+    if (k < K)
+      row = load_index(c.target, c.k == 0 ? t : t * c.index_stride + k, c.index64);
+    const f32x4 z = gather_logits<DT>(c, row < 0 ? 0 : row, at, wide);
+    if (lane % 16 == 0)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (k0 + lane / 16 * 4 + r < K) zs[k0 + lane / 16 * 4 + r] = z[r];
+  }
+  __syncthreads();
+  const float logs = logf(s), lse = m + logs;
+  if (c.k == 0) {
+    if (tid == 0) {
+      const float zy = zs[0];
+      // (m - zy) + log s: exact where the target is the largest logit
+      float loss = (m - zy) + logs;
+      if (c.smoothing != 0.0f) loss += c.smoothing * (zy - plain / (float)p.vocab);
+      if (c.z_loss != 0.0f) loss += c.z_loss * lse * lse;
+      c.loss[t] = loss;
+      c.lse[t] = lse;
+    }
+    return;
+  }
+  const float inv_temp = 1.0f / c.temperature;
+  float top = -INFINITY;
+  for (int k = tid; k < K; k += 256) {
+    const int64_t i = load_index(c.target, t * c.index_stride + k, c.index64);
+    const float l = i < 0 ? -INFINITY
+                          : load_any(c.teacher, t * c.logit_stride + k, c.teacher_dtype) * inv_temp;
+    c.logit[t * K + k] = i < 0 ? 0.0f : zs[k];
+    ls[k] = l;
+    top = fmaxf(top, l);
+  }
+  top = block_max<4>(top, red);
+  float total = 0.0f;
+  for (int k = tid; k < K; k += 256) total += exp_f(ls[k] - top);
+  total = block_sum<4>(total, red);
+  const float log_total = logf(total);
+  float kl = 0.0f;
+  for (int k = tid; k < K; k += 256) {
+    const float lp = ls[k] - top - log_total;
+    const float pk = exp_f(ls[k] - top) / total;
+    if (ls[k] != -INFINITY) kl += pk * (lp + (m - zs[k] * inv_temp));
+  }
+  kl = block_sum<4>(kl, red);
+  if (tid == 0) {
+    c.loss[t] = c.temperature * c.temperature * (kl + logs);
+    c.lse[t] = lse;
+  }
+}
+
+// ---- Rows: the gradient -----------------------------------------------------
+__global__ void __launch_bounds__(256) row_param_kernel(Call c) {
+  const Plan& p = c.plan;
+  const Head head = *reinterpret_cast<const Head*>(c.ws + p.o_head);
+  const int64_t r = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (r >= round_up_int(head.live, (int)kRowPad)) return;
+  RowParam rp = {};
+  rp.target = -1;
+  if (r < head.live) {
+    const int t = reinterpret_cast<const int*>(c.ws + p.o_rowmap)[r];
+    const float u = c.upstream[t * c.upstream_stride] * head.scale;
+    rp.lse = c.lse_in[t];
+    if (c.k == 0) {
+      rp.a = c.z_loss != 0.0f ? u * (1.0f + 2.0f * c.z_loss * rp.lse) : u;
+      rp.c = u * c.smoothing / (float)p.vocab;
+      rp.hit = u * (1.0f - c.smoothing);
+      rp.target = (int)load_index(c.target, t, c.index64);
+    } else {
+      rp.a = u * c.temperature;
+    }
+  }
+  reinterpret_cast<RowParam*>(c.ws + p.o_rowp)[r] = rp;
+}
+
+// Distillation: g at the teacher's entries that lie in the piece, written over
+// what the tile left there: formed in one go from the saved logit, so that it
+// too is rounded once. One wave a live row.
+template <int DT>
+__global__ void __launch_bounds__(64) entry_kernel(Call c, int64_t v0) {
+  const Plan& p = c.plan;
+  const int r = blockIdx.x, lane = threadIdx.x;
+  if (r >= reinterpret_cast<const Head*>(c.ws + p.o_head)->live) return;
+  __shared__ int idx[1024];
+  __shared__ float pk[1024];
+  const int64_t t = reinterpret_cast<const int*>(c.ws + p.o_rowmap)[r];
+  const RowParam rp = reinterpret_cast<const RowParam*>(c.ws + p.o_rowp)[r];
+  const float inv_temp = 1.0f / c.temperature;
+  float top = -INFINITY;
+  for (int k = lane; k < c.k; k += 64) {
+    const int64_t i = load_index(c.target, t * c.index_stride + k, c.index64);
+    const float l = i < 0 ? -INFINITY
+                          : load_any(c.teacher, t * c.logit_stride + k, c.teacher_dtype) * inv_temp;
+    idx[k] = i < 0 ? -1 : (int)i;
+    pk[k] = l;
+    top = fmaxf(top, l);
+  }
+  top = wave_max(top);
+  float total = 0.0f;
+  for (int k = lane; k < c.k; k += 64) {
+    const float e = exp_f(pk[k] - top);
+    pk[k] = e;
+    total += e;
+  }
+  total = wave_sum(total);
+  __syncthreads();
+  u16* g = reinterpret_cast<u16*>(c.ws + p.o_g) + (int64_t)r * p.piece;
+  for (int k = lane; k < c.k; k += 64) {
+    const int64_t m = idx[k] - v0;
+    if (idx[k] < 0 || m < 0 || m >= p.piece) continue;
+    float same = 0.0f;
+    for (int q = 0; q < c.k; ++q) same += idx[q] == idx[k] ? pk[q] : 0.0f;
+    const float z = c.logit_in[t * c.k + k] * inv_temp;
+    const float x = rp.a * (exp_f(z - rp.lse) - same / total);
+    if constexpr (DT == kF32) {
+      u16 parts[3];
+      split3(x, parts);
+      for (int s = 0; s < 3; ++s) g[s * p.rows * p.piece + m] = parts[s];
+    } else {
+      g[m] = DT == kBF16 ? bf16_bits(x) : f16_bits(x);
+    }
+  }
+}
+
+// Joins the slabs of dhidden's sum and writes every row, zeros where the row
+// took no part.
+template <int DT>
+__global__ void __launch_bounds__(256) dhidden_kernel(Call c, bool wide) {
+  const Plan& p = c.plan;
+  const int64_t t = blockIdx.x;
+  const int at = reinterpret_cast<const int*>(c.ws + p.o_pos)[t];
+  const float s = reinterpret_cast<const Head*>(c.ws + p.o_head)->inv_scale;
+  const float* acc = reinterpret_cast<const float*>(c.ws + p.o_acc) + (int64_t)at * p.dimp;
+  for (int k = threadIdx.x * 4; k < p.dim; k += 256 * 4) {
+    f32x4 x = {};
+    if (at >= 0) {
+      for (int q = 0; q < p.splits; ++q)
+        x += *reinterpret_cast<const f32x4*>(acc + q * p.rows * p.dimp + k);
+      x *= s;
+    }
+    if (k + 4 <= p.dim) {
+      store4<DT>(c.dhidden, t * c.dhidden_stride + k, x, wide);
+    } else {
+      for (int r = 0; r < 4 && k + r < p.dim; ++r)
+        store_value<DT>(c.dhidden, t * c.dhidden_stride + k + r, x[r]);
+    }
+  }
+}
+
+// ---- Launches -----------------------------------------------------------------
+bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+int64_t element(int dt) { return dt == kF32 ? 4 : 2; }
+
+// Whether every row of a tensor starts at a multiple of `n` elements' size.
+bool rows_aligned(const void* p, int64_t stride, int dt, int n) {
+  return aligned(p, (uintptr_t)(n * element(dt))) && stride % n == 0;
+}
+
+template <int DT, bool TA, bool TB, class Epi>
+void product(const Product& g, const Epi& epi, hipStream_t st) {
+  const dim3 grid((unsigned)((g.m + 127) / 128), (unsigned)((g.n + 127) / 128),
+                  (unsigned)g.splits);
+  product_kernel<DT, TA, TB, Epi><<<grid, 256, 0, st>>>(g, epi);
+}
+
+template <int DT>
+void rows_and_hidden(const Call& c, hipStream_t st) {
+  const Plan& p = c.plan;
+  if (c.k > 0 && p.tokens > 0)
+    classify_kernel<<<(unsigned)((p.tokens + 3) / 4), 256, 0, st>>>(
+        c, reinterpret_cast<uint8_t*>(c.ws + p.o_state));
+  scan_kernel<<<1, 1024, 0, st>>>(c);
+  if (p.tokens > 0)
+    pack_hidden_kernel<DT><<<(unsigned)p.rows, 256, 0, st>>>(
+        c, rows_aligned(c.hidden, c.hidden_stride, c.plan.dtype, 8));
+}
+
+// The piece's weights as an operand source: packed, or where they are.
+template <int DT>
+const u16* piece_weight(const Call& c, int64_t v0, int64_t* ld, hipStream_t st) {
+  const Plan& p = c.plan;
+  if (!p.pack_w) {
+    *ld = c.weight_stride;
+    return static_cast<const u16*>(c.weight) + v0 * c.weight_stride;
+  }
+  pack_weight_kernel<DT><<<(unsigned)p.piece, 256, 0, st>>>(
+      c, v0, rows_aligned(c.weight, c.weight_stride, p.dtype, 8));
+  *ld = p.dimp;
+  return reinterpret_cast<const u16*>(c.ws + p.o_w);
+}
+
+template <int DT>
+Product logits_product(const Call& c, const u16* w, int64_t ldw, int64_t real) {
+  const Plan& p = c.plan;
+  Product g{};
+  g.a = {w, p.piece * p.dimp, ldw, (int)real, (int)p.dimp};
+  g.b = {reinterpret_cast<const u16*>(c.ws + p.o_h), p.rows * p.dimp, p.dimp, (int)p.rows,
+         (int)p.dimp};
+  g.m = (int)real;
+  g.n = (int)p.rows;
+  g.inner = (int)p.dimp;
+  g.live_n = true;
+  g.segs = DT == kF32 ? kSegs : 1;
+  g.splits = 1;
+  g.head = reinterpret_cast<const Head*>(c.ws + p.o_head);
+  return g;
+}
+
+template <int DT>
+void loss_type(const Call& c, hipStream_t st) {
+  const Plan& p = c.plan;
+  rows_and_hidden<DT>(c, st);
+  for (int64_t v0 = 0; v0 < p.vocab; v0 += p.piece) {
+    int64_t ldw;
+    const u16* w = piece_weight<DT>(c, v0, &ldw, st);
+    const int64_t real = p.vocab - v0 < p.piece ? p.vocab - v0 : p.piece;
+    StatEpi epi{reinterpret_cast<float2*>(c.ws + p.o_stat),
+                c.smoothing != 0.0f ? reinterpret_cast<float*>(c.ws + p.o_sum) : nullptr,
+                p.stat_cols, 1.0f / c.temperature, (int)v0, (int)p.vocab};
+    product<DT, false, false>(logits_product<DT>(c, w, ldw, real), epi, st);
+  }
+  loss_kernel<DT><<<(unsigned)p.tokens, 256, 0, st>>>(
+      c, rows_aligned(c.weight, c.weight_stride, p.dtype, 8));
+}
+
+template <int DT>
+void grad_type(const Call& c, hipStream_t st) {
+  const Plan& p = c.plan;
+  const Head* head = reinterpret_cast<const Head*>(c.ws + p.o_head);
+  const u16* h = reinterpret_cast<const u16*>(c.ws + p.o_h);
+  u16* gbuf = reinterpret_cast<u16*>(c.ws + p.o_g);
+  rows_and_hidden<DT>(c, st);
+  row_param_kernel<<<(unsigned)((p.rows + 255) / 256), 256, 0, st>>>(c);
+  for (int64_t v0 = 0; v0 < p.vocab; v0 += p.piece) {
+    int64_t ldw;
+    const u16* w = piece_weight<DT>(c, v0, &ldw, st);
+    const int64_t real = p.vocab - v0 < p.piece ? p.vocab - v0 : p.piece;
+    // g of the piece
+    Product g = logits_product<DT>(c, w, ldw, real);
+    g.m = (int)p.piece;
+    GradEpi<DT> ge{reinterpret_cast<const RowParam*>(c.ws + p.o_rowp), gbuf, p.rows * p.piece,
+                   p.piece, 1.0f / c.temperature, (int)v0, (int)real};
+    product<DT, false, false>(g, ge, st);
+    if (c.k > 0 && p.tokens > 0) entry_kernel<DT><<<(unsigned)p.tokens, 64, 0, st>>>(c, v0);
+    // dhidden += g W: the inner index is the piece's vocabulary
+    if (c.dhidden != nullptr && p.tokens > 0) {
+      Product d{};
+      d.a = {w, p.piece * p.dimp, ldw, (int)p.dimp, (int)real};
+      d.b = {gbuf, p.rows * p.piece, p.piece, (int)p.rows, (int)p.piece};
+      d.m = (int)p.dimp;
+      d.n = (int)p.rows;
+      d.inner = (int)p.piece;
+      d.live_n = true;
+      d.segs = g.segs;
+      d.splits = p.splits;
+      d.head = head;
+      SumEpi se{reinterpret_cast<float*>(c.ws + p.o_acc), p.rows * p.dimp, p.dimp, (int)p.dimp,
+                v0 > 0};
+      product<DT, true, false>(d, se, st);
+    }
+    // dweight of the piece: the inner index is the live rows
+    if (c.dweight != nullptr) {
+      Product d{};
+      d.a = {h, p.rows * p.dimp, p.dimp, (int)p.dimp, (int)p.rows};
+      d.b = {gbuf, p.rows * p.piece, p.piece, (int)p.piece, (int)p.rows};
+      d.m = (int)p.dimp;
+      d.n = (int)real;
+      d.inner = (int)p.rows;
+      d.live_inner = true;
+      d.segs = g.segs;
+      d.splits = 1;
+      d.head = head;
+      WeightEpi<DT> we{c.dweight, c.dweight_stride, v0, (int)p.dim,
+                       rows_aligned(c.dweight, c.dweight_stride, p.dtype, 4), head};
+      product<DT, true, true>(d, we, st);
+    }
+  }
+  if (c.dhidden != nullptr && p.tokens > 0)
+    dhidden_kernel<DT><<<(unsigned)p.tokens, 256, 0, st>>>(
+        c, rows_aligned(c.dhidden, c.dhidden_stride, p.dtype, 4));
+}
+
+const char* status() {
+  const hipError_t e = hipGetLastError();
+  return e == hipSuccess ? nullptr : hipGetErrorString(e);
+}
+
+}  // namespace
+
+const char* launch_loss(const Call& c, void* stream) {
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  (void)hipGetLastError();
+  if (c.plan.dtype == kF32) loss_type<kF32>(c, st);
+  else if (c.plan.dtype == kBF16) loss_type<kBF16>(c, st);
+  else loss_type<kF16>(c, st);
+  return status();
+}
+
+const char* launch_grad(const Call& c, void* stream) {
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  (void)hipGetLastError();
+  if (c.plan.dtype == kF32) grad_type<kF32>(c, st);
+  else if (c.plan.dtype == kBF16) grad_type<kBF16>(c, st);
+  else grad_type<kF16>(c, st);
+  return status();
+}
+
+}  // namespace zloss
