@@ -136,7 +136,7 @@ __device__ __forceinline__ float wave_sum(float x) {
   return x;
 }
 
-__device__ __forceinline__ int round_up_int(int x, int m) { return (x + m - 1) / m * m; }
+__host__ __device__ __forceinline__ int round_up_int(int x, int m) { return (x + m - 1) / m * m; }
 
 // ---- Rows: which take part ------------------------------------------------
 // Distillation: one wave a row. 1 live, 0 empty, 2 bad.
@@ -297,6 +297,7 @@ struct Operand {
 struct Product {
   Operand a, b;
   int m, n;        // extents (n: the most there can be, where live_n)
+  int n_real;      // columns that mean something
   int inner;       // inner extent, a multiple of 64 (the most there can be, where live_inner)
   bool live_n, live_inner;  // the extent is the live count, rounded up to 64 for the inner one
   int segs;        // 1, or kSegs part products
@@ -304,76 +305,172 @@ struct Product {
   const Head* head;
 };
 
-// 128 x 128 tiles, inner steps of 32, through registers into LDS rows of
-// 32 + 8 elements (the pad spreads the rows over the banks). Four waves, each
-// 64 x 64 of the tile in 4 x 4 matrix instructions 16x16x32.
-template <int DT, bool TA, bool TB, class Epi>
-__global__ void __launch_bounds__(256) product_kernel(Product g, Epi epi) {
-  constexpr int BM = 128, BN = 128, BK = 32, LD = BK + 8;
-  __shared__ __attribute__((aligned(16))) u16 As[BM * LD];
-  __shared__ __attribute__((aligned(16))) u16 Bs[BN * LD];
+// 256 x BN tiles, inner steps of 64, two LDS stages that global memory is copied
+// into directly while the other is multiplied. Waves hold 128 x (BN / 4 or 32)
+// of the tile in matrix instructions 16x16x32.
+//
+// LDS holds a tile as it lies in memory, rows of 128 bytes (inner index
+// contiguous) or 512 bytes (rows contiguous), in 16-byte groups whose place in
+// their row is exchanged by a function of the row, so that the lanes of one read
+// fall on different banks. The copy writes lane after lane, so the exchange is
+// made in the addresses it reads from. A transposed tile is turned by the
+// transposing LDS read, four inner steps of 16 rows a time.
+typedef __attribute__((address_space(3))) char lds_char;
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+template <int BN>
+struct Shape {
+  static constexpr int kWaveN = BN == 256 ? 64 : 32;
+  static constexpr int kWaves = 2 * (BN / kWaveN);
+  static constexpr int kThreads = 64 * kWaves;
+  static constexpr int kStage = (256 + BN) * 128;  // bytes
+};
+
+// Byte offsets, from the tile's corner (r0 < o.rows: a tile starts on a real row), that lane `l` of wave `w` copies from
+// with its i-th instruction of 64 groups.
+template <bool T, int R>
+__device__ __forceinline__ uint32_t copy_offset(const Operand& o, int r0, int instr, int lane) {
+  if constexpr (!T) {
+    const int r = instr * 8 + lane / 8;
+    const int group = (lane % 8) ^ (lane / 8);
+    return (uint32_t)(min(r0 + r, o.rows - 1) - r0) * (uint32_t)(o.ld * 2) + group * 16;
+  } else {
+    static_assert(R == 256, "two inner steps an instruction");
+    const int k = instr * 2 + lane / 32;
+    const int turn = (k & 3) | ((k >> 3) & 1) << 2;
+    const int group = (lane % 32) ^ (turn << 1);
+    return (uint32_t)k * (uint32_t)(o.ld * 2) + (uint32_t)(min(r0 + group * 8, o.rows - 8) - r0) * 2;
+  }
+}
+
+__device__ __forceinline__ void copy_to_lds(const char* base, uint32_t offset, lds_char* to) {
+  __builtin_amdgcn_global_load_lds(
+      (const __attribute__((address_space(1))) void*)(base + offset),
+      (__attribute__((address_space(3))) void*)to, 16, 0, 0);
+}
+
+// The operand registers of one matrix instruction: 16 rows from `at`, inner
+// steps 32 ks + lane / 16 * 8 + 0..7.
+template <bool T>
+__device__ __forceinline__ u32x4 fragment(lds_char* tile, int at, int ks, int lane) {
+  if constexpr (!T) {
+    const int off = (at + lane % 16) * 128 + (((ks * 4 + lane / 16) ^ (lane & 7)) * 16);
+    return *reinterpret_cast<__attribute__((address_space(3))) u32x4*>(tile + off);
+  } else {
+    const int i = lane % 16, g = lane / 16;
+    const int turn = (i / 4) | (g & 1) << 2;
+    const int off = (ks * 32 + g * 8 + i / 4) * 512 + (((at / 16) ^ turn) * 32) + (i % 4) * 8;
+    typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        reinterpret_cast<lds_s16x4*>(tile + off));
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        reinterpret_cast<lds_s16x4*>(tile + off + 4 * 512));
+    const u32x2 a = __builtin_bit_cast(u32x2, lo), b = __builtin_bit_cast(u32x2, hi);
+    return u32x4{a[0], a[1], b[0], b[1]};
+  }
+}
+
+template <int DT, bool TA, bool TB, int BN, class Epi>
+__global__ void __launch_bounds__(Shape<BN>::kThreads, 2) product_kernel(Product g, Epi epi) {
+  using S = Shape<BN>;
+  constexpr int MI = 8, NJ = S::kWaveN / 16;
+  constexpr int kCopyA = 32 / S::kWaves, kCopyB = BN / 8 / S::kWaves;
+  __shared__ __attribute__((aligned(1024))) char smem[2 * S::kStage];
+  lds_char* lds = (lds_char*)smem;
+
   const int live = g.head->live;
   const int n_ext = g.live_n ? live : g.n;
   const int inner = g.live_inner ? round_up_int(live, 64) : g.inner;
-  const int m0 = blockIdx.x * BM, n0 = blockIdx.y * BN;
-  if (n0 >= n_ext) return;
-  const int chunk = round_up_int((inner + g.splits - 1) / g.splits, 64);
-  const int k_lo = min(inner, (int)blockIdx.z * chunk), k_hi = min(inner, k_lo + chunk);
-  const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
-  const int wm = (wave & 1) * 64, wn = (wave >> 1) * 64;
+  // Tiles are numbered in strips four columns wide, and each of the chip's eight
+  // dies (blocks go to them in turn) gets a run of them, so that the tiles in
+  // flight on a die share rows and columns in its cache.
+  const int mt = (g.m + 255) / 256, nt = (n_ext + BN - 1) / BN;
+  const int total = mt * nt * g.splits, run = (total + 7) / 8;
+  int id = (int)blockIdx.x;
+  if (id / 8 >= run) return;
+  id = (id % 8) * run + id / 8;
+  if (id >= total) return;
+  const int split = id / (mt * nt);
+  id -= split * mt * nt;
+  const int strip = id / (4 * mt), wide = min(4, nt - strip * 4);
+  id -= strip * 4 * mt;
+  const int m0 = id / wide * 256, n0 = (strip * 4 + id % wide) * BN;
 
-  f32x4 acc[4][4] = {};
-  const auto load = [&](const Operand& o, const u16* base, bool t, int r0, int k0, int part) {
-    const int id = tid + part * 256;  // 512 groups of 8 elements a tile
-    if (!t) {
-      const int r = min(r0 + id / 4, o.rows - 1), k = k0 + (id % 4) * 8;
-      return *reinterpret_cast<const u32x4*>(base + (int64_t)r * o.ld + k);
-    }
-    const int k = min(k0 + id / 16, o.steps - 1), r = min(r0 + (id % 16) * 8, o.rows - 8);
-    return *reinterpret_cast<const u32x4*>(base + (int64_t)k * o.ld + r);
+  const int chunk = round_up_int((inner + g.splits - 1) / g.splits, 64);
+  const int k_lo = min(inner, split * chunk), k_hi = min(inner, k_lo + chunk);
+  const int steps = (k_hi - k_lo) / 64, all = steps * g.segs;
+  const int tid = threadIdx.x, lane = tid % 64;
+  const int wave = __builtin_amdgcn_readfirstlane(tid / 64);
+  const int wm = (wave & 1) * 128, wn = (wave >> 1) * S::kWaveN;
+
+  uint32_t oa[kCopyA], ob[kCopyB];
+#pragma unroll
+  for (int i = 0; i < kCopyA; ++i)
+    oa[i] = copy_offset<TA, 256>(g.a, m0, wave * kCopyA + i, lane);
+#pragma unroll
+  for (int i = 0; i < kCopyB; ++i)
+    ob[i] = copy_offset<TB, BN>(g.b, n0, wave * kCopyB + i, lane);
+  const auto corner = [&](const Operand& o, bool t, int r0, int part) {
+    return reinterpret_cast<const char*>(o.p + part * o.plane +
+                                         (t ? k_lo * o.ld + r0 : r0 * o.ld + k_lo));
   };
-  const auto keep = [&](u16* s, bool t, int part, u32x4 v) {
-    const int id = tid + part * 256;
-    if (!t) {
-      *reinterpret_cast<u32x4*>(s + (id / 4) * LD + (id % 4) * 8) = v;
+  const int64_t step_a = TA ? g.a.ld * 128 : 128, step_b = TB ? g.b.ld * 128 : 128;
+  const char* pa = corner(g.a, TA, m0, g.segs > 1 ? kSegA[0] : 0);
+  const char* pb = corner(g.b, TB, n0, g.segs > 1 ? kSegB[0] : 0);
+  int seg = 0, at = 0;  // the next step to copy
+  const auto copy = [&](int stage) {
+    lds_char* to = lds + stage * S::kStage;
+    if (TA && k_lo + at * 64 + 64 > g.a.steps) {
+      // the weight's last rows: there are no more, and the other operand holds zeros
+#pragma unroll
+      for (int i = 0; i < kCopyA; ++i) {
+        const int k = (wave * kCopyA + i) * 2 + lane / 32;
+        const int over = max(0, k_lo + at * 64 + k - (g.a.steps - 1));
+        copy_to_lds(pa, oa[i] - (uint32_t)over * (uint32_t)(g.a.ld * 2),
+                    to + (wave * kCopyA + i) * 1024);
+      }
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        s[((id % 16) * 8 + i) * LD + id / 16] = (u16)(v[i / 2] >> (16 * (i % 2)));
+      for (int i = 0; i < kCopyA; ++i)
+        copy_to_lds(pa, oa[i], to + (wave * kCopyA + i) * 1024);
+    }
+#pragma unroll
+    for (int i = 0; i < kCopyB; ++i)
+      copy_to_lds(pb, ob[i], to + 32768 + (wave * kCopyB + i) * 1024);
+    pa += step_a;
+    pb += step_b;
+    if (++at == steps) {
+      at = 0;
+      if (++seg < g.segs) {
+        pa = corner(g.a, TA, m0, kSegA[seg]);
+        pb = corner(g.b, TB, n0, kSegB[seg]);
+      }
     }
   };
-  for (int seg = 0; seg < g.segs; ++seg) {
-    const u16* a = g.a.p + (g.segs > 1 ? kSegA[seg] * g.a.plane : 0);
-    const u16* b = g.b.p + (g.segs > 1 ? kSegB[seg] * g.b.plane : 0);
-    for (int k0 = k_lo; k0 < k_hi; k0 += BK) {
-      u32x4 va[2], vb[2];
+
+  f32x4 acc[MI][NJ] = {};
+  if (all > 0) copy(0);
+  for (int it = 0; it < all; ++it) {
+    // this step's copies have landed, and every wave has read all of the other stage
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    if (it + 1 < all) copy((it + 1) & 1);
+    lds_char* ta = lds + (it & 1) * S::kStage;
+    lds_char* tb = ta + 32768;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        va[i] = load(g.a, a, TA, m0, k0, i);
-        vb[i] = load(g.b, b, TB, n0, k0, i);
-      }
-      __syncthreads();
+    for (int ks = 0; ks < 2; ++ks) {
+      u32x4 fa[MI], fb[NJ];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        keep(As, TA, i, va[i]);
-        keep(Bs, TB, i, vb[i]);
-      }
-      __syncthreads();
-      u32x4 fa[4], fb[4];
+      for (int j = 0; j < NJ; ++j) fb[j] = fragment<TB>(tb, wn + j * 16, ks, lane);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        fa[i] = *reinterpret_cast<const u32x4*>(As + (wm + i * 16 + lane % 16) * LD +
-                                                lane / 16 * 8);
-        fb[i] = *reinterpret_cast<const u32x4*>(Bs + (wn + i * 16 + lane % 16) * LD +
-                                                lane / 16 * 8);
-      }
+      for (int i = 0; i < MI; ++i) fa[i] = fragment<TA>(ta, wm + i * 16, ks, lane);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < MI; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = mfma<DT>(fa[i], fb[j], acc[i][j]);
+        for (int j = 0; j < NJ; ++j) acc[i][j] = mfma<DT>(fa[i], fb[j], acc[i][j]);
     }
   }
-  epi.template tile<4, 4>(m0 + wm, n0 + wn, n_ext, (int)blockIdx.z, acc);
+  epi.template tile<MI, NJ>(m0 + wm, n0 + wn, n_ext, split, acc);
 }
 
 // ---- What happens to a tile -------------------------------------------------
@@ -431,8 +528,9 @@ struct StatEpi {
 };
 
 // Gradient: the same tile becomes g, [rows][ld] with the vocabulary
-// contiguous. Rows beyond the live ones and columns beyond the vocabulary hold
-// zeros, so that the products over g need not know either.
+// contiguous. Rows beyond the live ones and columns beyond the vocabulary, up to
+// the end of the last tile, hold zeros, so that the products over g need not
+// know either.
 template <int DT>
 struct GradEpi {
   const RowParam* rows;
@@ -780,11 +878,21 @@ bool rows_aligned(const void* p, int64_t stride, int dt, int n) {
   return aligned(p, (uintptr_t)(n * element(dt))) && stride % n == 0;
 }
 
+template <int DT, bool TA, bool TB, int BN, class Epi>
+void product_tiles(const Product& g, const Epi& epi, hipStream_t st) {
+  const int64_t total = (int64_t)((g.m + 255) / 256) * ((g.n + BN - 1) / BN) * g.splits;
+  product_kernel<DT, TA, TB, BN, Epi>
+      <<<(unsigned)((total + 7) / 8 * 8), Shape<BN>::kThreads, 0, st>>>(g, epi);
+}
+
+// Columns are tokens (few of them take narrower tiles) or, where the right
+// operand is transposed, vocabulary.
 template <int DT, bool TA, bool TB, class Epi>
 void product(const Product& g, const Epi& epi, hipStream_t st) {
-  const dim3 grid((unsigned)((g.m + 127) / 128), (unsigned)((g.n + 127) / 128),
-                  (unsigned)g.splits);
-  product_kernel<DT, TA, TB, Epi><<<grid, 256, 0, st>>>(g, epi);
+  if constexpr (!TB) {
+    if (g.n_real <= 64) return product_tiles<DT, TA, TB, 64, Epi>(g, epi, st);
+  }
+  product_tiles<DT, TA, TB, 256, Epi>(g, epi, st);
 }
 
 template <int DT>
@@ -822,6 +930,7 @@ Product logits_product(const Call& c, const u16* w, int64_t ldw, int64_t real) {
          (int)p.dimp};
   g.m = (int)real;
   g.n = (int)p.rows;
+  g.n_real = (int)p.tokens;
   g.inner = (int)p.dimp;
   g.live_n = true;
   g.segs = DT == kF32 ? kSegs : 1;
@@ -861,7 +970,6 @@ void grad_type(const Call& c, hipStream_t st) {
     const int64_t real = p.vocab - v0 < p.piece ? p.vocab - v0 : p.piece;
     // g of the piece
     Product g = logits_product<DT>(c, w, ldw, real);
-    g.m = (int)p.piece;
     GradEpi<DT> ge{reinterpret_cast<const RowParam*>(c.ws + p.o_rowp), gbuf, p.rows * p.piece,
                    p.piece, 1.0f / c.temperature, (int)v0, (int)real};
     product<DT, false, false>(g, ge, st);
@@ -873,7 +981,8 @@ void grad_type(const Call& c, hipStream_t st) {
       d.b = {gbuf, p.rows * p.piece, p.piece, (int)p.rows, (int)p.piece};
       d.m = (int)p.dimp;
       d.n = (int)p.rows;
-      d.inner = (int)p.piece;
+      d.n_real = (int)p.tokens;
+      d.inner = round_up_int((int)real, 64);
       d.live_n = true;
       d.segs = g.segs;
       d.splits = p.splits;

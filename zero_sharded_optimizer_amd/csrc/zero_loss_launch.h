@@ -15,7 +15,7 @@ constexpr int64_t kRowPad = 256;  // token rows
 constexpr int64_t kVocPad = 256;  // vocabulary rows of a piece
 constexpr int64_t kDimPad = 64;   // the products' inner step
 // Vocabulary rows one entry of the softmax partials covers.
-constexpr int64_t kStatRows = 64;
+constexpr int64_t kStatRows = 128;
 
 // Sizes and workspace offsets of one call, made by the ABI layer.
 struct Plan {
