@@ -343,10 +343,18 @@ __device__ __forceinline__ uint32_t copy_offset(const Operand& o, int r0, int in
   }
 }
 
-__device__ __forceinline__ void copy_to_lds(const char* base, uint32_t offset, lds_char* to) {
-  __builtin_amdgcn_global_load_lds(
-      (const __attribute__((address_space(1))) void*)(base + offset),
-      (__attribute__((address_space(3))) void*)to, 16, 0, 0);
+// 16 bytes a lane from base + offset to LDS, lane after lane from `to` (both the
+// same in the whole wave). The compiler does not see it as a load, and so does
+// not hold up the transposing reads, which it cannot tell apart from the stage
+// that is being written, until it has landed: the waits are written out below.
+__device__ __forceinline__ void copy_to_lds(const char* base, uint32_t offset, uint32_t to) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dwordx4 %1, %2"
+      :
+      : "s"(to), "v"(offset), "s"(base)
+      : "memory");
 }
 
 // The operand registers of one matrix instruction: 16 rows from `at`, inner
@@ -377,6 +385,7 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, 2) product_kernel(Product
   constexpr int kCopyA = 32 / S::kWaves, kCopyB = BN / 8 / S::kWaves;
   __shared__ __attribute__((aligned(1024))) char smem[2 * S::kStage];
   lds_char* lds = (lds_char*)smem;
+  const uint32_t lds_at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds);
 
   const int live = g.head->live;
   const int n_ext = g.live_n ? live : g.n;
@@ -419,7 +428,7 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, 2) product_kernel(Product
   const char* pb = corner(g.b, TB, n0, g.segs > 1 ? kSegB[0] : 0);
   int seg = 0, at = 0;  // the next step to copy
   const auto copy = [&](int stage) {
-    lds_char* to = lds + stage * S::kStage;
+    const uint32_t to = lds_at + stage * S::kStage;
     if (TA && k_lo + at * 64 + 64 > g.a.steps) {
       // the weight's last rows: there are no more, and the other operand holds zeros
 #pragma unroll
@@ -449,26 +458,54 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, 2) product_kernel(Product
   };
 
   f32x4 acc[MI][NJ] = {};
-  if (all > 0) copy(0);
-  for (int it = 0; it < all; ++it) {
-    // this step's copies have landed, and every wave has read all of the other stage
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    if (it + 1 < all) copy((it + 1) & 1);
-    lds_char* ta = lds + (it & 1) * S::kStage;
-    lds_char* tb = ta + 32768;
+  u32x4 fa0[MI], fb0[NJ], fa1[MI], fb1[NJ];
+  const auto read = [&](int stage, int ks, u32x4 (&fa)[MI], u32x4 (&fb)[NJ]) {
+    lds_char* ta = lds + stage * S::kStage;
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-      u32x4 fa[MI], fb[NJ];
+    for (int j = 0; j < NJ; ++j) fb[j] = fragment<TB>(ta + 32768, wn + j * 16, ks, lane);
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) fb[j] = fragment<TB>(tb, wn + j * 16, ks, lane);
+    for (int i = 0; i < MI; ++i) fa[i] = fragment<TA>(ta, wm + i * 16, ks, lane);
+  };
+  const auto multiply = [&](u32x4 (&fa)[MI], u32x4 (&fb)[NJ]) {
 #pragma unroll
-      for (int i = 0; i < MI; ++i) fa[i] = fragment<TA>(ta, wm + i * 16, ks, lane);
+    for (int i = 0; i < MI; ++i)
 #pragma unroll
-      for (int i = 0; i < MI; ++i)
+      for (int j = 0; j < NJ; ++j) acc[i][j] = mfma<DT>(fa[i], fb[j], acc[i][j]);
+  };
+  // Asks the compiler to spread a half step's LDS reads between the matrix
+  // instructions of the half before it.
+  const auto spread = [&]() {
+    constexpr int reads = MI * (TA ? 2 : 1) + NJ * (TB ? 2 : 1), each = TA ? 2 : 1;
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) acc[i][j] = mfma<DT>(fa[i], fb[j], acc[i][j]);
+    for (int q = 0; q < reads / each; ++q) {
+      __builtin_amdgcn_sched_group_barrier(0x008, NJ / 2, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, each, 0);
     }
+  };
+  if (all > 0) {
+    // Each half step's operands are read while the half before is multiplied, and
+    // the block meets between them: there the second half is in registers, so a
+    // stage may be copied over, and the matrix units have work on both sides.
+    copy(0);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    if (all > 1) copy(1);
+    read(0, 0, fa0, fb0);
+    for (int it = 0; it + 1 < all; ++it) {
+      read(it & 1, 1, fa1, fb1);
+      multiply(fa0, fb0);
+      spread();
+      // the next stage has landed, and every wave has read all of this one
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+      __builtin_amdgcn_s_barrier();
+      if (it + 2 < all) copy(it & 1);
+      read((it + 1) & 1, 0, fa0, fb0);
+      multiply(fa1, fb1);
+      spread();
+    }
+    read((all - 1) & 1, 1, fa1, fb1);
+    multiply(fa0, fb0);
+    multiply(fa1, fb1);
   }
   epi.template tile<MI, NJ>(m0 + wm, n0 + wn, n_ext, split, acc);
 }
