@@ -14,6 +14,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "zero_loss_launch.h"
 
@@ -427,25 +428,25 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, 2) product_kernel(Product
   const char* pa = corner(g.a, TA, m0, g.segs > 1 ? kSegA[0] : 0);
   const char* pb = corner(g.b, TB, n0, g.segs > 1 ? kSegB[0] : 0);
   int seg = 0, at = 0;  // the next step to copy
-  const auto copy = [&](int stage) {
+  // Instruction i of a step's copies, A's first.
+  const auto copy_part = [&](int stage, int i) {
     const uint32_t to = lds_at + stage * S::kStage;
+    if (i < kCopyA) copy_to_lds(pa, oa[i], to + (wave * kCopyA + i) * 1024);
+    else copy_to_lds(pb, ob[i - kCopyA], to + 32768 + (wave * kCopyB + i - kCopyA) * 1024);
+  };
+  const auto before_copy = [&]() {
     if (TA && k_lo + at * 64 + 64 > g.a.steps) {
       // the weight's last rows: there are no more, and the other operand holds zeros
 #pragma unroll
       for (int i = 0; i < kCopyA; ++i) {
         const int k = (wave * kCopyA + i) * 2 + lane / 32;
         const int over = max(0, k_lo + at * 64 + k - (g.a.steps - 1));
-        copy_to_lds(pa, oa[i] - (uint32_t)over * (uint32_t)(g.a.ld * 2),
-                    to + (wave * kCopyA + i) * 1024);
+        oa[i] = copy_offset<TA, 256>(g.a, m0, wave * kCopyA + i, lane) -
+                (uint32_t)over * (uint32_t)(g.a.ld * 2);
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < kCopyA; ++i)
-        copy_to_lds(pa, oa[i], to + (wave * kCopyA + i) * 1024);
     }
-#pragma unroll
-    for (int i = 0; i < kCopyB; ++i)
-      copy_to_lds(pb, ob[i], to + 32768 + (wave * kCopyB + i) * 1024);
+  };
+  const auto after_copy = [&]() {
     pa += step_a;
     pb += step_b;
     if (++at == steps) {
@@ -453,59 +454,85 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, 2) product_kernel(Product
       if (++seg < g.segs) {
         pa = corner(g.a, TA, m0, kSegA[seg]);
         pb = corner(g.b, TB, n0, kSegB[seg]);
+        if constexpr (TA) {
+#pragma unroll
+          for (int i = 0; i < kCopyA; ++i)
+            oa[i] = copy_offset<TA, 256>(g.a, m0, wave * kCopyA + i, lane);
+        }
       }
     }
+  };
+  const auto copy = [&](int stage) {
+    before_copy();
+#pragma unroll
+    for (int i = 0; i < kCopyA + kCopyB; ++i) copy_part(stage, i);
+    after_copy();
   };
 
   f32x4 acc[MI][NJ] = {};
   u32x4 fa0[MI], fb0[NJ], fa1[MI], fb1[NJ];
-  const auto read = [&](int stage, int ks, u32x4 (&fa)[MI], u32x4 (&fb)[NJ]) {
+  // Operand q of a half step, in the order the matrix instructions want them.
+  const auto read_part = [&](int stage, int ks, int q, u32x4 (&fa)[MI], u32x4 (&fb)[NJ]) {
     lds_char* ta = lds + stage * S::kStage;
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) fb[j] = fragment<TB>(ta + 32768, wn + j * 16, ks, lane);
-#pragma unroll
-    for (int i = 0; i < MI; ++i) fa[i] = fragment<TA>(ta, wm + i * 16, ks, lane);
+    if (q == 1) fa[0] = fragment<TA>(ta, wm, ks, lane);
+    else if (q <= NJ) fb[q == 0 ? 0 : q - 1] = fragment<TB>(ta + 32768, wn + (q == 0 ? 0 : q - 1) * 16, ks, lane);
+    else fa[q - NJ] = fragment<TA>(ta, wm + (q - NJ) * 16, ks, lane);
   };
-  const auto multiply = [&](u32x4 (&fa)[MI], u32x4 (&fb)[NJ]) {
+  // Multiplies one half step, row by row of the wave's tile, and between the rows
+  // reads the next half's operands (read_stage >= 0) and copies the next free
+  // stage (copy_stage >= 0): both are issued in the matrix instructions' shadow.
+  const auto half = [&](u32x4 (&fa)[MI], u32x4 (&fb)[NJ], int read_stage, int ks,
+                        u32x4 (&na)[MI], u32x4 (&nb)[NJ], auto copies, int copy_stage) {
+    constexpr int kReads = MI + NJ, kFirst = MI - 2;  // the last two rows cover the latency
 #pragma unroll
-    for (int i = 0; i < MI; ++i)
+    for (int i = 0; i < MI; ++i) {
 #pragma unroll
       for (int j = 0; j < NJ; ++j) acc[i][j] = mfma<DT>(fa[i], fb[j], acc[i][j]);
-  };
-  // Asks the compiler to spread a half step's LDS reads between the matrix
-  // instructions of the half before it.
-  const auto spread = [&]() {
-    constexpr int reads = MI * (TA ? 2 : 1) + NJ * (TB ? 2 : 1), each = TA ? 2 : 1;
+      if (read_stage >= 0) {
 #pragma unroll
-    for (int q = 0; q < reads / each; ++q) {
-      __builtin_amdgcn_sched_group_barrier(0x008, NJ / 2, 0);
-      __builtin_amdgcn_sched_group_barrier(0x100, each, 0);
+        for (int q = i * kReads / kFirst; q < min(kReads, (i + 1) * kReads / kFirst); ++q)
+          read_part(read_stage, ks, q, na, nb);
+      }
+      if constexpr (decltype(copies)::value) {
+        constexpr int n = kCopyA + kCopyB;
+#pragma unroll
+        for (int q = i * n / MI; q < (i + 1) * n / MI; ++q) copy_part(copy_stage, q);
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
+  };
+  using Yes = std::true_type;
+  using No = std::false_type;
+  // A stage's copies have landed, and every wave has read all of the other stage.
+  const auto meet = [&]() {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
   };
   if (all > 0) {
     // Each half step's operands are read while the half before is multiplied, and
-    // the block meets between them: there the second half is in registers, so a
+    // the block meets between them: there the second half is in registers, so the
     // stage may be copied over, and the matrix units have work on both sides.
     copy(0);
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();
+    meet();
     if (all > 1) copy(1);
-    read(0, 0, fa0, fb0);
-    for (int it = 0; it + 1 < all; ++it) {
-      read(it & 1, 1, fa1, fb1);
-      multiply(fa0, fb0);
-      spread();
-      // the next stage has landed, and every wave has read all of this one
-      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-      __builtin_amdgcn_s_barrier();
-      if (it + 2 < all) copy(it & 1);
-      read((it + 1) & 1, 0, fa0, fb0);
-      multiply(fa1, fb1);
-      spread();
+#pragma unroll
+    for (int q = 0; q < MI + NJ; ++q) read_part(0, 0, q, fa0, fb0);
+    int it = 0;
+    for (; it + 2 < all; ++it) {
+      half(fa0, fb0, it & 1, 1, fa1, fb1, No{}, 0);
+      meet();
+      before_copy();
+      half(fa1, fb1, (it + 1) & 1, 0, fa0, fb0, Yes{}, it & 1);
+      after_copy();
     }
-    read((all - 1) & 1, 1, fa1, fb1);
-    multiply(fa0, fb0);
-    multiply(fa1, fb1);
+    if (it + 1 < all) {
+      half(fa0, fb0, it & 1, 1, fa1, fb1, No{}, 0);
+      meet();
+      half(fa1, fb1, (it + 1) & 1, 0, fa0, fb0, No{}, 0);
+      ++it;
+    }
+    half(fa0, fb0, it & 1, 1, fa1, fb1, No{}, 0);
+    half(fa1, fb1, -1, 0, fa0, fb0, No{}, 0);
   }
   epi.template tile<MI, NJ>(m0 + wm, n0 + wn, n_ext, split, acc);
 }
