@@ -700,28 +700,58 @@ struct WeightEpi {
 };
 
 // ---- Rows: the losses -------------------------------------------------------
-// The logits of up to 16 vocabulary rows (one per lane % 16) against one live
-// row, by the same matrix instructions in the same order as the tiles', so that
-// they are the same bits as the ones in the softmax's sum: in a loss near zero
-// the two have to cancel. Lane l gets rows l / 16 * 4 + 0..3.
+// The targets' logits, by the same matrix instructions in the same order as the
+// tiles', so that they are the same bits as the ones in the softmax's sum: in a
+// loss near zero the two have to cancel. One wave has 16 (row, entry) pairs, one
+// per lane % 16: sixteen live rows with their one target each, or sixteen
+// entries of one row. It multiplies their 16 weight rows with their 16 hidden
+// rows and keeps the diagonal. Pairs outside the piece are left for theirs.
 template <int DT>
-__device__ __forceinline__ f32x4 gather_logits(const Call& c, int64_t row, int live_row,
-                                               bool wide) {
+__global__ void __launch_bounds__(256) gather_kernel(Call c, const u16* w, int64_t ldw,
+                                                     int64_t v0, int real) {
   const Plan& p = c.plan;
-  const int lane = threadIdx.x % 64;
-  const u16* h = reinterpret_cast<const u16*>(c.ws + p.o_h) + (int64_t)live_row * p.dimp;
-  const int64_t at = row * c.weight_stride;
+  const int live = reinterpret_cast<const Head*>(c.ws + p.o_head)->live;
+  const int K = c.k == 0 ? 1 : c.k, per_row = (K + 15) / 16;
+  const int lane = threadIdx.x % 64, q = lane % 16;
+  const int64_t id = (int64_t)blockIdx.x * 4 + threadIdx.x / 64;
+  const int row = (int)(c.k == 0 ? id * 16 + q : id / per_row);
+  const int k = c.k == 0 ? 0 : (int)(id % per_row) * 16 + q;
+  int64_t m = -1;  // the pair's row in the piece
+  int64_t t = 0;
+  if (row < live && k < K) {
+    t = reinterpret_cast<const int*>(c.ws + p.o_rowmap)[row];
+    m = load_index(c.target, c.k == 0 ? t : t * c.index_stride + k, c.index64);
+    m = m < 0 ? -1 : m - v0;  // padding has no weight row
+  }
+  const bool mine = m >= 0 && m < real;
+  if (!__any(mine)) return;
+  const u16* h = reinterpret_cast<const u16*>(c.ws + p.o_h) +
+                 (int64_t)min(row, live - 1) * p.dimp + lane / 16 * 8;
+  const u16* a = w + (mine ? m : 0) * ldw + lane / 16 * 8;
   f32x4 acc = {};
   for (int seg = 0; seg < (DT == kF32 ? kSegs : 1); ++seg) {
-    const int sa = DT == kF32 ? kSegA[seg] : 0, sb = DT == kF32 ? kSegB[seg] : 0;
-    for (int k = lane / 16 * 8; k < p.dimp; k += 32) {
-      u32x4 a[3];
-      pack8<DT>(c.weight, at, k, (int)p.dim, wide, a);
-      const u32x4 b = *reinterpret_cast<const u32x4*>(h + sb * p.rows * p.dimp + k);
-      acc = mfma<DT>(DT == kF32 ? (sa == 0 ? a[0] : sa == 1 ? a[1] : a[2]) : a[0], b, acc);
+    const u16* pa = a + (DT == kF32 ? kSegA[seg] * p.piece * p.dimp : 0);
+    const u16* pb = h + (DT == kF32 ? kSegB[seg] * p.rows * p.dimp : 0);
+    int k0 = 0;
+    for (; k0 + 256 <= p.dimp; k0 += 256) {  // eight loads on their way at a time
+      u32x4 va[8], vb[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        va[i] = *reinterpret_cast<const u32x4*>(pa + k0 + i * 32);
+        vb[i] = *reinterpret_cast<const u32x4*>(pb + k0 + i * 32);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc = mfma<DT>(va[i], vb[i], acc);
     }
+    for (; k0 < p.dimp; k0 += 32)
+      acc = mfma<DT>(*reinterpret_cast<const u32x4*>(pa + k0),
+                     *reinterpret_cast<const u32x4*>(pb + k0), acc);
   }
-  return acc;
+  // lane l holds rows l / 16 * 4 + 0..3 of column l % 16
+  if (mine && q / 4 == lane / 16) {
+    const float z = q % 4 == 0 ? acc[0] : q % 4 == 1 ? acc[1] : q % 4 == 2 ? acc[2] : acc[3];
+    (c.k == 0 ? reinterpret_cast<float*>(c.ws + p.o_entry) : c.logit)[t * K + k] = z;
+  }
 }
 
 template <int N>
@@ -744,16 +774,13 @@ __device__ __forceinline__ float block_sum(float x, float* s) {
   return x;
 }
 
-// One block a token: joins the partials, gathers the targets' logits, writes
-// the loss.
-template <int DT>
-__global__ void __launch_bounds__(256) loss_kernel(Call c, bool wide) {
+// One block a token: joins the partials and writes the loss.
+__global__ void __launch_bounds__(256) loss_kernel(Call c) {
   const Plan& p = c.plan;
   const int64_t t = blockIdx.x;
-  const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
+  const int tid = threadIdx.x;
   const int K = c.k == 0 ? 1 : c.k;
   __shared__ float red[4];
-  __shared__ float zs[1024];
   __shared__ float ls[1024];
   const int at = reinterpret_cast<const int*>(c.ws + p.o_pos)[t];
   if (at < 0) {
@@ -780,19 +807,7 @@ __global__ void __launch_bounds__(256) loss_kernel(Call c, bool wide) {
     for (int i = tid; i < cols; i += 256) plain += sum[i];
     plain = block_sum<4>(plain, red);
   }
-  // the targets' logits, 16 a wave
-  for (int k0 = wave * 16; k0 < K; k0 += 64) {
-    const int k = k0 + lane % 16;
-    int64_t row = -1;
-    if (k < K)
-      row = load_index(c.target, c.k == 0 ? t : t * c.index_stride + k, c.index64);
-    const f32x4 z = gather_logits<DT>(c, row < 0 ? 0 : row, at, wide);
-    if (lane % 16 == 0)
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        if (k0 + lane / 16 * 4 + r < K) zs[k0 + lane / 16 * 4 + r] = z[r];
-  }
-  __syncthreads();
+  const float* zs = (c.k == 0 ? reinterpret_cast<const float*>(c.ws + p.o_entry) : c.logit) + t * K;
   const float logs = logf(s), lse = m + logs;
   if (c.k == 0) {
     if (tid == 0) {
@@ -812,7 +827,7 @@ __global__ void __launch_bounds__(256) loss_kernel(Call c, bool wide) {
     const int64_t i = load_index(c.target, t * c.index_stride + k, c.index64);
     const float l = i < 0 ? -INFINITY
                           : load_any(c.teacher, t * c.logit_stride + k, c.teacher_dtype) * inv_temp;
-    c.logit[t * K + k] = i < 0 ? 0.0f : zs[k];
+    if (i < 0) c.logit[t * K + k] = 0.0f;
     ls[k] = l;
     top = fmaxf(top, l);
   }
@@ -908,27 +923,34 @@ __global__ void __launch_bounds__(64) entry_kernel(Call c, int64_t v0) {
 }
 
 // Joins the slabs of dhidden's sum and writes every row, zeros where the row
-// took no part.
+// took no part. A wave has 256 columns of a row.
 template <int DT>
-__global__ void __launch_bounds__(256) dhidden_kernel(Call c, bool wide) {
+__global__ void __launch_bounds__(64) dhidden_kernel(Call c, bool wide) {
   const Plan& p = c.plan;
   const int64_t t = blockIdx.x;
   const int at = reinterpret_cast<const int*>(c.ws + p.o_pos)[t];
   const float s = reinterpret_cast<const Head*>(c.ws + p.o_head)->inv_scale;
-  const float* acc = reinterpret_cast<const float*>(c.ws + p.o_acc) + (int64_t)at * p.dimp;
-  for (int k = threadIdx.x * 4; k < p.dim; k += 256 * 4) {
-    f32x4 x = {};
-    if (at >= 0) {
-      for (int q = 0; q < p.splits; ++q)
-        x += *reinterpret_cast<const f32x4*>(acc + q * p.rows * p.dimp + k);
-      x *= s;
+  const int k = (int)blockIdx.y * 256 + threadIdx.x * 4;
+  if (k >= p.dim) return;
+  f32x4 x = {};
+  if (at >= 0) {
+    const float* acc = reinterpret_cast<const float*>(c.ws + p.o_acc) + (int64_t)at * p.dimp + k;
+    for (int q = 0; q < p.splits; q += 8) {
+      f32x4 v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        v[i] = *reinterpret_cast<const f32x4*>(acc + min(q + i, p.splits - 1) * p.rows * p.dimp);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (q + i < p.splits) x += v[i];
     }
-    if (k + 4 <= p.dim) {
-      store4<DT>(c.dhidden, t * c.dhidden_stride + k, x, wide);
-    } else {
-      for (int r = 0; r < 4 && k + r < p.dim; ++r)
-        store_value<DT>(c.dhidden, t * c.dhidden_stride + k + r, x[r]);
-    }
+    x *= s;
+  }
+  if (k + 4 <= p.dim) {
+    store4<DT>(c.dhidden, t * c.dhidden_stride + k, x, wide);
+  } else {
+    for (int r = 0; r < 4 && k + r < p.dim; ++r)
+      store_value<DT>(c.dhidden, t * c.dhidden_stride + k + r, x[r]);
   }
 }
 
@@ -1015,9 +1037,10 @@ void loss_type(const Call& c, hipStream_t st) {
                 c.smoothing != 0.0f ? reinterpret_cast<float*>(c.ws + p.o_sum) : nullptr,
                 p.stat_cols, 1.0f / c.temperature, (int)v0, (int)p.vocab};
     product<DT, false, false>(logits_product<DT>(c, w, ldw, real), epi, st);
+    const int64_t waves = c.k == 0 ? (p.tokens + 15) / 16 : p.tokens * ((c.k + 15) / 16);
+    gather_kernel<DT><<<(unsigned)((waves + 3) / 4), 256, 0, st>>>(c, w, ldw, v0, (int)real);
   }
-  loss_kernel<DT><<<(unsigned)p.tokens, 256, 0, st>>>(
-      c, rows_aligned(c.weight, c.weight_stride, p.dtype, 8));
+  loss_kernel<<<(unsigned)p.tokens, 256, 0, st>>>(c);
 }
 
 template <int DT>
@@ -1073,7 +1096,7 @@ void grad_type(const Call& c, hipStream_t st) {
     }
   }
   if (c.dhidden != nullptr && p.tokens > 0)
-    dhidden_kernel<DT><<<(unsigned)p.tokens, 256, 0, st>>>(
+    dhidden_kernel<DT><<<dim3((unsigned)p.tokens, (unsigned)((p.dim + 255) / 256)), 64, 0, st>>>(
         c, rows_aligned(c.dhidden, c.dhidden_stride, p.dtype, 4));
 }
 

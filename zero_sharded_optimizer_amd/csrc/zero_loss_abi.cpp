@@ -127,6 +127,7 @@ zloss::Plan make_plan(const zero_head& h, bool grad) {
   if (!grad) {
     p.o_stat = take(p.rows * p.stat_cols * 8);
     p.o_sum = take(p.rows * p.stat_cols * 4);
+    p.o_entry = take(p.rows * 4);
   } else {
     p.o_rowp = take(p.rows * 32);
     p.o_g = take(p.planes * p.rows * p.piece * 2);

@@ -38,6 +38,7 @@ struct Plan {
   size_t o_w;        // 16-bit [planes][piece][dimp] when pack_w
   size_t o_stat;     // float2 [rows][stat_cols] (forward)
   size_t o_sum;      // float [rows][stat_cols] (forward): sums of the logits
+  size_t o_entry;    // float [tokens] (cross entropy, forward): the targets' logits
   size_t o_rowp;     // RowParam[rows] (gradient)
   size_t o_g;        // 16-bit [planes][rows][piece] (gradient)
   size_t o_acc;      // float [splits][rows][dimp] (gradient)
