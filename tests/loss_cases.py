@@ -4,15 +4,18 @@ The reference is the losses' definition in float64 with torch's elementary
 operations, on whatever device the inputs are on.
 
 Bounds. Let u = eps/2 of the tensors' type, e = 2^-24. A logit is a sum of D
-products in fp32 (six times as many for fp32 inputs, whose parts drop at most
-2^-25 of a product): its error is at most dz = (N D + 16) e sum|h||W|, N = 6 or 1.
-The log-sum-exp moves by at most the largest dz of the row plus the roundings of
-its own sums, (V/64 + 64 + 40) e relative in the sum and a few e of its value.
-One term of the logits' gradient is then off by |a| p (dz + dlse + 40 e) before
-it is rounded once (u, and in fp16 at least 2^-39 of the largest upstream
-gradient, where its scaled form turns subnormal), and the products over it add
-(N K + 16) e sum|g||x| before the result is rounded once more (u, and in fp16
-2^-25 absolute).
+products in fp32 (three times as many for fp32 inputs, whose two fp16 parts each
+lose at most e of a value and drop at most e of a product, 3 e together, or 2^-40
+of the tensor's largest value where that is more): its error is at most
+dz = (N D + 16) e sum|h||W|, N = 3 or 1, and 2^-40 (max|h| sum|W| + max|W| sum|h|)
+for fp32. The log-sum-exp moves by at most the largest dz of the row plus the
+roundings of its own sums, (V/64 + 64 + 40) e relative in the sum and a few e of
+its value. One term of the logits' gradient is then off by |a| p (dz + dlse + 40 e)
+before it is rounded once (u; in fp16 and in fp32's fp16 parts at least 2^-39 of
+the largest upstream gradient, where the scaled form turns subnormal), and the
+products over it add (N K + 16) e sum|g||x|, in fp32 also 2^-40 of the largest
+|x| times sum|g|, before the result is rounded once more (u, and in fp16 2^-25
+absolute).
 """
 import math
 
@@ -47,7 +50,7 @@ def reference(c, smoothing=0.0, z_loss=0.0, temperature=1.0, ignore_index=-100):
     dt = c["hidden"].dtype
     T, D = c["hidden"].shape
     V = c["weight"].shape[0]
-    N = 6 if dt == torch.float32 else 1
+    N = 3 if dt == torch.float32 else 1
     u = torch.finfo(dt).eps / 2
     tau = temperature
     if "target" in c:
@@ -88,7 +91,12 @@ def reference(c, smoothing=0.0, z_loss=0.0, temperature=1.0, ignore_index=-100):
     loss = torch.where(bad, math.nan, loss)
     lse = torch.where(live, lse, 0.0)
     # bounds
+    f32 = dt == torch.float32
     dz = ((N * D + 16) * E) * (h.abs() @ w.abs().T) / tau
+    if f32 and T:
+        hmax, wmax = float(h.abs().max()), float(w.abs().max())
+        dz = dz + 2.0 ** -40 / tau * (hmax * w.abs().sum(1)[None, :]
+                                      + wmax * h.abs().sum(1)[:, None])
     top = dz.amax(1)
     zmax = z.abs().amax(1)
     dlse = top + (V / 64 + 104) * E + 4 * E * (lse.abs() + zmax)
@@ -100,14 +108,17 @@ def reference(c, smoothing=0.0, z_loss=0.0, temperature=1.0, ignore_index=-100):
         dloss = dloss + smoothing * (V / 64 + 80) * E * z.abs().mean(1)
     dp = a.abs()[:, None] * p * (dz + dlse[:, None] + 40 * E) \
         + 8 * E * (a.abs()[:, None] * (p + want) + up.abs()[:, None] * want)
-    floor = up.abs().max() * tau * 2.0 ** -39 if dt == torch.float16 and T else 0.0
-    dg = dp + u * g.abs() * (0.0 if dt == torch.float32 else 1.0) + floor
+    floor = up.abs().max() * tau * 2.0 ** -39 if dt != torch.bfloat16 and T else 0.0
+    dg = dp + u * g.abs() * (3.0 if f32 else 1.0) + floor
     dg = torch.where(live[:, None], dg, 0.0)
     ga = g.abs()
     dh, dw = g @ w, g.T @ h
     tiny = 2.0 ** -25 if dt == torch.float16 else 0.0
     bh = dg @ w.abs() + (N * V + 16) * E * (ga @ w.abs())
     bw = dg.T @ h.abs() + (N * T + 16) * E * (ga.T @ h.abs())
+    if f32 and T:
+        bh = bh + 2.0 ** -40 * wmax * ga.sum(1)[:, None]
+        bw = bw + 2.0 ** -40 * hmax * ga.sum(0)[:, None]
     bh = bh + u * (dh.abs() + bh) + tiny + 1e-37
     bw = bw + u * (dw.abs() + bw) + tiny + 1e-37
     bounds = {"loss": dloss + 1e-37, "lse": dlse + 1e-37, "dh": bh, "dw": bw}

@@ -9,8 +9,13 @@
 //             tile to softmax partials, the gradient turns it into g
 //   dhidden   += g W,   dweight = g^T hidden    (gradient, per piece)
 // Every product is one tiled kernel over 16-bit operands with fp32 sums. fp32
-// inputs go through it as three bf16 parts each (x = hi + mid + lo, exact to
-// 2^-26) and six of the nine part products, small ones first.
+// values go through it as two fp16 parts, x = hi + lo, each tensor scaled by the
+// power of two that brings its largest magnitude near 2^15: hi has 11 bits, lo
+// the next 11 and its sign one more, so a value keeps 24 bits as long as it is
+// above 2^-17 of the largest, and an absolute 2^-40 of the largest below that.
+// Three part products are summed, small ones first; the fourth, lo lo, is below
+// 2^-24 of the whole, as is a rounding in fp32. (Three bf16 parts need no scale,
+// but six products for the same error: twice the time.)
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -35,7 +40,21 @@ struct Head {
   int live;         // rows that take part
   float scale;      // power of two that g is held at
   float inv_scale;
+  // fp32: the bits of the largest magnitude in the live rows of hidden, and in the
+  // weight. (Non-negative floats order as their bits do, NaN above all.)
+  uint32_t top_h, top_w;
 };
+
+// The power of two that brings `top` to [2^14, 2^15), within 2^+-100, and 1 for
+// zero, infinities and NaN.
+__device__ __forceinline__ int scale_exponent(float top) {
+  if (!(top > 0.0f && top < INFINITY)) return 0;
+  const int e = 14 - ilogbf(top);
+  return e < -100 ? -100 : e > 100 ? 100 : e;
+}
+__device__ __forceinline__ int scale_exponent(uint32_t bits) {
+  return scale_exponent(__builtin_bit_cast(float, bits));
+}
 
 // Per live row, for the logits' gradient g = a exp(z - lse) - c - hit [j = target].
 struct RowParam {
@@ -46,9 +65,10 @@ struct RowParam {
 static_assert(sizeof(RowParam) == 32, "the plan counts 32 bytes a row");
 
 // The part products of fp32 operands: (left part, right part), small ones first.
-constexpr int kSegs = 6;
-__device__ __constant__ const int kSegA[kSegs] = {1, 2, 0, 1, 0, 0};
-__device__ __constant__ const int kSegB[kSegs] = {1, 0, 2, 0, 1, 0};
+constexpr int kParts = 2;
+constexpr int kSegs = 3;
+__device__ __forceinline__ int seg_a(int seg) { return seg == 0 ? 1 : 0; }
+__device__ __forceinline__ int seg_b(int seg) { return seg == 1 ? 1 : 0; }
 
 // ---- Values ---------------------------------------------------------------
 __device__ __forceinline__ u16 bf16_bits(float x) { return __builtin_bit_cast(u16, (__bf16)x); }
@@ -60,15 +80,12 @@ __device__ __forceinline__ float f16_float(u16 b) {
   return (float)__builtin_bit_cast(_Float16, b);
 }
 
-// x = p[0] + p[1] + p[2] in bf16 parts. An infinity or NaN is its first part
-// alone (the remainder would be NaN).
-__device__ __forceinline__ void split3(float x, u16 p[3]) {
-  p[0] = bf16_bits(x);
-  const float hi = bf16_float(p[0]);
-  const bool fine = __builtin_isfinite(hi);
-  const float r = fine ? x - hi : 0.0f;
-  p[1] = bf16_bits(r);
-  p[2] = bf16_bits(r - bf16_float(p[1]));
+// x = p[0] + p[1] in fp16 parts. An infinity or NaN is its first part alone (the
+// remainder would be NaN).
+__device__ __forceinline__ void split2(float x, u16 p[kParts]) {
+  p[0] = f16_bits(x);
+  const float hi = f16_float(p[0]);
+  p[1] = f16_bits(__builtin_isfinite(hi) ? x - hi : 0.0f);
 }
 
 template <int DT>
@@ -118,7 +135,7 @@ __device__ __forceinline__ float exp_f(float x) { return __builtin_amdgcn_exp2f(
 
 template <int DT>
 __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
-  if constexpr (DT == kF16)
+  if constexpr (DT != kBF16)
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
                                                   __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
   else
@@ -210,22 +227,50 @@ __global__ void __launch_bounds__(1024) scan_kernel(Call c) {
   __syncthreads();
   if (tid == 0) {
     for (int w = 0; w < 16; ++w) top = fmaxf(top, tops[w]);
-    int e = 0;
-    if (top > 0.0f && top < INFINITY) {
-      e = 14 - ilogbf(top);
-      e = e < -100 ? -100 : e > 100 ? 100 : e;
-    }
+    const int e = scale_exponent(top);
     head->live = base;
     head->scale = ldexpf(1.0f, e);
     head->inv_scale = ldexpf(1.0f, -e);
+    head->top_h = head->top_w = 0;
   }
 }
 
 // ---- Packing --------------------------------------------------------------
+// fp32: the largest magnitudes of the live rows of hidden (blocks from `first_h`
+// on) and of the weight, 16 rows a block. Largest of largest in any order is the
+// same number, so the atomics leave nothing to chance.
+__global__ void __launch_bounds__(256) top_kernel(Call c, int first_h, bool wide_h, bool wide_w) {
+  const Plan& p = c.plan;
+  Head* head = reinterpret_cast<Head*>(c.ws + p.o_head);
+  const bool is_h = (int)blockIdx.x >= first_h;
+  const int64_t r0 = (int64_t)(is_h ? blockIdx.x - first_h : blockIdx.x) * 16;
+  const int64_t rows = is_h ? head->live : p.vocab;
+  const int wave = threadIdx.x / 64, lane = threadIdx.x % 64;
+  uint32_t top = 0;
+  for (int64_t r = r0 + wave; r < min(rows, r0 + 16); r += 4) {
+    const int64_t row = is_h ? reinterpret_cast<const int*>(c.ws + p.o_rowmap)[r] : r;
+    const uint32_t* x = static_cast<const uint32_t*>(is_h ? c.hidden : c.weight) +
+                        row * (is_h ? c.hidden_stride : c.weight_stride);
+    int k = 0;
+    if (is_h ? wide_h : wide_w) {
+      for (k = lane * 4; k + 4 <= p.dim; k += 256) {
+        const u32x4 v = *reinterpret_cast<const u32x4*>(x + k);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = max(top, v[i] & 0x7fffffffu);
+      }
+      k = (int)p.dim / 4 * 4;
+    }
+    for (k += lane; k < p.dim; k += 64) top = max(top, x[k] & 0x7fffffffu);
+  }
+#pragma unroll
+  for (int d = 32; d; d >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
+  if (lane == 0 && top != 0) atomicMax(is_h ? &head->top_h : &head->top_w, top);
+}
+
 // Eight elements from column k of a row, zero beyond `dim`, as 16-bit parts.
 template <int DT>
 __device__ __forceinline__ void pack8(const void* src, int64_t at, int k, int dim, bool wide,
-                                      u32x4 out[3]) {
+                                      float scale, u32x4 out[kParts]) {
   if constexpr (DT != kF32) {
     if (wide && k + 8 <= dim) {
       out[0] = *reinterpret_cast<const u32x4*>(static_cast<const u16*>(src) + at + k);
@@ -236,16 +281,26 @@ __device__ __forceinline__ void pack8(const void* src, int64_t at, int k, int di
     for (int i = 0; i < 8; ++i) b[i] = k + i < dim ? static_cast<const u16*>(src)[at + k + i] : 0;
     out[0] = *reinterpret_cast<const u32x4*>(b);
   } else {
-    u16 parts[3][8];
+    const float* x = static_cast<const float*>(src) + at + k;
+    float v[8];
+    if (wide && k + 8 <= dim) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        *reinterpret_cast<f32x4*>(v + 4 * i) = *reinterpret_cast<const f32x4*>(x + 4 * i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = k + i < dim ? x[i] : 0.0f;
+    }
+    u16 parts[kParts][8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      u16 p[3];
-      split3(k + i < dim ? static_cast<const float*>(src)[at + k + i] : 0.0f, p);
+      u16 p[kParts];
+      split2(v[i] * scale, p);
 #pragma unroll
-      for (int s = 0; s < 3; ++s) parts[s][i] = p[s];
+      for (int s = 0; s < kParts; ++s) parts[s][i] = p[s];
     }
 #pragma unroll
-    for (int s = 0; s < 3; ++s) out[s] = *reinterpret_cast<const u32x4*>(parts[s]);
+    for (int s = 0; s < kParts; ++s) out[s] = *reinterpret_cast<const u32x4*>(parts[s]);
   }
 }
 
@@ -253,17 +308,19 @@ __device__ __forceinline__ void pack8(const void* src, int64_t at, int k, int di
 template <int DT>
 __global__ void __launch_bounds__(256) pack_hidden_kernel(Call c, bool wide) {
   const Plan& p = c.plan;
-  const int live = reinterpret_cast<const Head*>(c.ws + p.o_head)->live;
+  const Head* head = reinterpret_cast<const Head*>(c.ws + p.o_head);
+  const int live = head->live;
   const int r = blockIdx.x;
   if (r >= round_up_int(live, (int)kRowPad)) return;
   u16* dst = reinterpret_cast<u16*>(c.ws + p.o_h) + (int64_t)r * p.dimp;
   const bool real = r < live;
+  const float scale = DT == kF32 ? ldexpf(1.0f, scale_exponent(head->top_h)) : 1.0f;
   const int64_t at =
       real ? reinterpret_cast<const int*>(c.ws + p.o_rowmap)[r] * c.hidden_stride : 0;
   for (int k = threadIdx.x * 8; k < p.dimp; k += 256 * 8) {
-    u32x4 v[3] = {};
-    if (real) pack8<DT>(c.hidden, at, k, (int)p.dim, wide, v);
-    for (int s = 0; s < (DT == kF32 ? 3 : 1); ++s)
+    u32x4 v[kParts] = {};
+    if (real) pack8<DT>(c.hidden, at, k, (int)p.dim, wide, scale, v);
+    for (int s = 0; s < (DT == kF32 ? kParts : 1); ++s)
       *reinterpret_cast<u32x4*>(dst + s * p.rows * p.dimp + k) = v[s];
   }
 }
@@ -275,12 +332,33 @@ __global__ void __launch_bounds__(256) pack_weight_kernel(Call c, int64_t v0, bo
   const int64_t r = blockIdx.x;
   u16* dst = reinterpret_cast<u16*>(c.ws + p.o_w) + r * p.dimp;
   const bool real = v0 + r < p.vocab;
+  const float scale =
+      DT == kF32
+          ? ldexpf(1.0f, scale_exponent(reinterpret_cast<const Head*>(c.ws + p.o_head)->top_w))
+          : 1.0f;
   for (int k = threadIdx.x * 8; k < p.dimp; k += 256 * 8) {
-    u32x4 v[3] = {};
-    if (real) pack8<DT>(c.weight, (v0 + r) * c.weight_stride, k, (int)p.dim, wide, v);
-    for (int s = 0; s < (DT == kF32 ? 3 : 1); ++s)
+    u32x4 v[kParts] = {};
+    if (real) pack8<DT>(c.weight, (v0 + r) * c.weight_stride, k, (int)p.dim, wide, scale, v);
+    for (int s = 0; s < (DT == kF32 ? kParts : 1); ++s)
       *reinterpret_cast<u32x4*>(dst + s * p.piece * p.dimp + k) = v[s];
   }
+}
+
+// What a sum over scaled operands is multiplied by to undo their scales: one
+// factor each, since the two together may leave fp32's range.
+template <int DT>
+__device__ __forceinline__ float undo_h(const Head* head) {
+  return DT == kF32 ? ldexpf(1.0f, -scale_exponent(head->top_h)) : 1.0f;
+}
+template <int DT>
+__device__ __forceinline__ float undo_w(const Head* head) {
+  return DT == kF32 ? ldexpf(1.0f, -scale_exponent(head->top_w)) : 1.0f;
+}
+// A logit over the temperature, from its sum. The factors other than the
+// temperature's are exact.
+template <int DT>
+__device__ __forceinline__ float logit_of(float sum, float undo_h, float undo_w, float inv_temp) {
+  return DT == kF32 ? sum * undo_h * undo_w * inv_temp : sum * inv_temp;
 }
 
 // ---- The product ----------------------------------------------------------
@@ -425,8 +503,8 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, 2) product_kernel(Product
                                          (t ? k_lo * o.ld + r0 : r0 * o.ld + k_lo));
   };
   const int64_t step_a = TA ? g.a.ld * 128 : 128, step_b = TB ? g.b.ld * 128 : 128;
-  const char* pa = corner(g.a, TA, m0, g.segs > 1 ? kSegA[0] : 0);
-  const char* pb = corner(g.b, TB, n0, g.segs > 1 ? kSegB[0] : 0);
+  const char* pa = corner(g.a, TA, m0, g.segs > 1 ? seg_a(0) : 0);
+  const char* pb = corner(g.b, TB, n0, g.segs > 1 ? seg_b(0) : 0);
   int seg = 0, at = 0;  // the next step to copy
   // Instruction i of a step's copies, A's first.
   const auto copy_part = [&](int stage, int i) {
@@ -452,8 +530,8 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, 2) product_kernel(Product
     if (++at == steps) {
       at = 0;
       if (++seg < g.segs) {
-        pa = corner(g.a, TA, m0, kSegA[seg]);
-        pb = corner(g.b, TB, n0, kSegB[seg]);
+        pa = corner(g.a, TA, m0, seg_a(seg));
+        pb = corner(g.b, TB, n0, seg_b(seg));
         if constexpr (TA) {
 #pragma unroll
           for (int i = 0; i < kCopyA; ++i)
@@ -544,7 +622,9 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, 2) product_kernel(Product
 // Forward: the tile's rows m are vocabulary, its columns n live rows. Each wave
 // leaves the largest logit, the sum of exponentials and the sum of logits of
 // its stretch of the vocabulary.
+template <int DT>
 struct StatEpi {
+  const Head* head;
   float2* stat;
   float* sum;       // nullptr where nobody asks for it
   int64_t cols;     // partials per row
@@ -557,6 +637,7 @@ struct StatEpi {
     const int lane = threadIdx.x % 64;
     const int m_hi = vocab - m_base;
     if (m0 >= round_up_int(m_hi, (int)kStatRows)) return;
+    const float uh = undo_h<DT>(head), uw = undo_w<DT>(head);
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
       float top = -INFINITY, total = 0.0f, plain = 0.0f;
@@ -565,7 +646,7 @@ struct StatEpi {
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const bool in = m0 + i * 16 + lane / 16 * 4 + r < m_hi;
-          const float z = in ? acc[i][j][r] * inv_temp : -INFINITY;
+          const float z = in ? logit_of<DT>(acc[i][j][r], uh, uw, inv_temp) : -INFINITY;
           acc[i][j][r] = z;
           plain += in ? z : 0.0f;
           top = fmaxf(top, z);
@@ -597,6 +678,7 @@ struct StatEpi {
 // know either.
 template <int DT>
 struct GradEpi {
+  const Head* head;
   const RowParam* rows;
   u16* g;
   int64_t plane, ld;
@@ -605,6 +687,7 @@ struct GradEpi {
   template <int MI, int NJ>
   __device__ __forceinline__ void tile(int m0, int n0, int n_ext, int, f32x4 (&acc)[MI][NJ]) {
     const int lane = threadIdx.x % 64;
+    const float uh = undo_h<DT>(head), uw = undo_w<DT>(head);
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
       const int n = n0 + j * 16 + lane % 16;
@@ -614,23 +697,23 @@ struct GradEpi {
 #pragma unroll
       for (int i = 0; i < MI; ++i) {
         const int m = m0 + i * 16 + lane / 16 * 4;
-        u16 parts[3][4];
+        u16 parts[kParts][4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          float x = rp.a * exp_f(acc[i][j][r] * inv_temp - rp.lse) - rp.c;
+          float x = rp.a * exp_f(logit_of<DT>(acc[i][j][r], uh, uw, inv_temp) - rp.lse) - rp.c;
           if (m + r == at) x -= rp.hit;
           x = real && m + r < m_ext ? x : 0.0f;
           if constexpr (DT == kF32) {
-            u16 p[3];
-            split3(x, p);
-            for (int s = 0; s < 3; ++s) parts[s][r] = p[s];
+            u16 p[kParts];
+            split2(x, p);
+            for (int s = 0; s < kParts; ++s) parts[s][r] = p[s];
           } else {
             parts[0][r] = DT == kBF16 ? bf16_bits(x) : f16_bits(x);
           }
         }
         if (m < ld) {
 #pragma unroll
-          for (int s = 0; s < (DT == kF32 ? 3 : 1); ++s)
+          for (int s = 0; s < (DT == kF32 ? kParts : 1); ++s)
             *reinterpret_cast<u32x2*>(g + s * plane + n * ld + m) =
                 u32x2{parts[s][0] | (uint32_t)parts[s][1] << 16,
                       parts[s][2] | (uint32_t)parts[s][3] << 16};
@@ -678,7 +761,7 @@ struct WeightEpi {
   template <int MI, int NJ>
   __device__ __forceinline__ void tile(int m0, int n0, int n_ext, int, f32x4 (&acc)[MI][NJ]) {
     const int lane = threadIdx.x % 64;
-    const float s = head->inv_scale;
+    const float s = head->inv_scale, uh = undo_h<DT>(head);
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
       const int n = n0 + j * 16 + lane % 16;
@@ -686,7 +769,7 @@ struct WeightEpi {
 #pragma unroll
       for (int i = 0; i < MI; ++i) {
         const int m = m0 + i * 16 + lane / 16 * 4;
-        const f32x4 x = acc[i][j] * s;
+        const f32x4 x = acc[i][j] * uh * s;
         if (m + 4 <= m_ext) {
           store4<DT>(out, (v0 + n) * ld + m, x, wide);
         } else {
@@ -730,8 +813,8 @@ __global__ void __launch_bounds__(256) gather_kernel(Call c, const u16* w, int64
   const u16* a = w + (mine ? m : 0) * ldw + lane / 16 * 8;
   f32x4 acc = {};
   for (int seg = 0; seg < (DT == kF32 ? kSegs : 1); ++seg) {
-    const u16* pa = a + (DT == kF32 ? kSegA[seg] * p.piece * p.dimp : 0);
-    const u16* pb = h + (DT == kF32 ? kSegB[seg] * p.rows * p.dimp : 0);
+    const u16* pa = a + (DT == kF32 ? seg_a(seg) * p.piece * p.dimp : 0);
+    const u16* pb = h + (DT == kF32 ? seg_b(seg) * p.rows * p.dimp : 0);
     int k0 = 0;
     for (; k0 + 256 <= p.dimp; k0 += 256) {  // eight loads on their way at a time
       u32x4 va[8], vb[8];
@@ -749,7 +832,9 @@ __global__ void __launch_bounds__(256) gather_kernel(Call c, const u16* w, int64
   }
   // lane l holds rows l / 16 * 4 + 0..3 of column l % 16
   if (mine && q / 4 == lane / 16) {
-    const float z = q % 4 == 0 ? acc[0] : q % 4 == 1 ? acc[1] : q % 4 == 2 ? acc[2] : acc[3];
+    const float sum = q % 4 == 0 ? acc[0] : q % 4 == 1 ? acc[1] : q % 4 == 2 ? acc[2] : acc[3];
+    const Head* head = reinterpret_cast<const Head*>(c.ws + p.o_head);
+    const float z = logit_of<DT>(sum, undo_h<DT>(head), undo_w<DT>(head), 1.0f);
     (c.k == 0 ? reinterpret_cast<float*>(c.ws + p.o_entry) : c.logit)[t * K + k] = z;
   }
 }
@@ -913,9 +998,9 @@ __global__ void __launch_bounds__(64) entry_kernel(Call c, int64_t v0) {
     const float z = c.logit_in[t * c.k + k] * inv_temp;
     const float x = rp.a * (exp_f(z - rp.lse) - same / total);
     if constexpr (DT == kF32) {
-      u16 parts[3];
-      split3(x, parts);
-      for (int s = 0; s < 3; ++s) g[s * p.rows * p.piece + m] = parts[s];
+      u16 parts[kParts];
+      split2(x, parts);
+      for (int s = 0; s < kParts; ++s) g[s * p.rows * p.piece + m] = parts[s];
     } else {
       g[m] = DT == kBF16 ? bf16_bits(x) : f16_bits(x);
     }
@@ -929,7 +1014,7 @@ __global__ void __launch_bounds__(64) dhidden_kernel(Call c, bool wide) {
   const Plan& p = c.plan;
   const int64_t t = blockIdx.x;
   const int at = reinterpret_cast<const int*>(c.ws + p.o_pos)[t];
-  const float s = reinterpret_cast<const Head*>(c.ws + p.o_head)->inv_scale;
+  const Head* head = reinterpret_cast<const Head*>(c.ws + p.o_head);
   const int k = (int)blockIdx.y * 256 + threadIdx.x * 4;
   if (k >= p.dim) return;
   f32x4 x = {};
@@ -944,7 +1029,7 @@ __global__ void __launch_bounds__(64) dhidden_kernel(Call c, bool wide) {
       for (int i = 0; i < 8; ++i)
         if (q + i < p.splits) x += v[i];
     }
-    x *= s;
+    x = x * undo_w<DT>(head) * head->inv_scale;
   }
   if (k + 4 <= p.dim) {
     store4<DT>(c.dhidden, t * c.dhidden_stride + k, x, wide);
@@ -988,9 +1073,15 @@ void rows_and_hidden(const Call& c, hipStream_t st) {
     classify_kernel<<<(unsigned)((p.tokens + 3) / 4), 256, 0, st>>>(
         c, reinterpret_cast<uint8_t*>(c.ws + p.o_state));
   scan_kernel<<<1, 1024, 0, st>>>(c);
+  if (DT == kF32) {
+    const int first_h = (int)((p.vocab + 15) / 16);
+    top_kernel<<<(unsigned)(first_h + (p.tokens + 15) / 16), 256, 0, st>>>(
+        c, first_h, rows_aligned(c.hidden, c.hidden_stride, p.dtype, 4),
+        rows_aligned(c.weight, c.weight_stride, p.dtype, 4));
+  }
   if (p.tokens > 0)
     pack_hidden_kernel<DT><<<(unsigned)p.rows, 256, 0, st>>>(
-        c, rows_aligned(c.hidden, c.hidden_stride, c.plan.dtype, 8));
+        c, rows_aligned(c.hidden, c.hidden_stride, p.dtype, 16 / (int)element(p.dtype)));
 }
 
 // The piece's weights as an operand source: packed, or where they are.
@@ -1002,7 +1093,7 @@ const u16* piece_weight(const Call& c, int64_t v0, int64_t* ld, hipStream_t st) 
     return static_cast<const u16*>(c.weight) + v0 * c.weight_stride;
   }
   pack_weight_kernel<DT><<<(unsigned)p.piece, 256, 0, st>>>(
-      c, v0, rows_aligned(c.weight, c.weight_stride, p.dtype, 8));
+      c, v0, rows_aligned(c.weight, c.weight_stride, p.dtype, 16 / (int)element(p.dtype)));
   *ld = p.dimp;
   return reinterpret_cast<const u16*>(c.ws + p.o_w);
 }
@@ -1033,7 +1124,8 @@ void loss_type(const Call& c, hipStream_t st) {
     int64_t ldw;
     const u16* w = piece_weight<DT>(c, v0, &ldw, st);
     const int64_t real = p.vocab - v0 < p.piece ? p.vocab - v0 : p.piece;
-    StatEpi epi{reinterpret_cast<float2*>(c.ws + p.o_stat),
+    StatEpi<DT> epi{reinterpret_cast<const Head*>(c.ws + p.o_head),
+                    reinterpret_cast<float2*>(c.ws + p.o_stat),
                 c.smoothing != 0.0f ? reinterpret_cast<float*>(c.ws + p.o_sum) : nullptr,
                 p.stat_cols, 1.0f / c.temperature, (int)v0, (int)p.vocab};
     product<DT, false, false>(logits_product<DT>(c, w, ldw, real), epi, st);
@@ -1057,7 +1149,7 @@ void grad_type(const Call& c, hipStream_t st) {
     const int64_t real = p.vocab - v0 < p.piece ? p.vocab - v0 : p.piece;
     // g of the piece
     Product g = logits_product<DT>(c, w, ldw, real);
-    GradEpi<DT> ge{reinterpret_cast<const RowParam*>(c.ws + p.o_rowp), gbuf, p.rows * p.piece,
+    GradEpi<DT> ge{head, reinterpret_cast<const RowParam*>(c.ws + p.o_rowp), gbuf, p.rows * p.piece,
                    p.piece, 1.0f / c.temperature, (int)v0, (int)real};
     product<DT, false, false>(g, ge, st);
     if (c.k > 0 && p.tokens > 0) entry_kernel<DT><<<(unsigned)p.tokens, 64, 0, st>>>(c, v0);

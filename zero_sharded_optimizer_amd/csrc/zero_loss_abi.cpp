@@ -87,7 +87,7 @@ zloss::Plan make_plan(const zero_head& h, bool grad) {
   p.vocab = h.vocab;
   p.dim = h.dim;
   p.dtype = h.dtype;
-  p.planes = h.dtype == ZERO_LOSS_F32 ? 3 : 1;
+  p.planes = h.dtype == ZERO_LOSS_F32 ? 2 : 1;
   p.grad = grad;
   p.rows = round_up(std::max<int64_t>(h.tokens, 1), zloss::kRowPad);
   p.dimp = round_up(h.dim, zloss::kDimPad);

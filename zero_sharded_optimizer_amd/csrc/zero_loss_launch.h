@@ -21,7 +21,7 @@ constexpr int64_t kStatRows = 128;
 struct Plan {
   int64_t tokens, vocab, dim;
   int dtype;
-  int planes;        // 16-bit parts per value: 3 for fp32, else 1
+  int planes;        // 16-bit parts per value: 2 for fp32, else 1
   bool grad;
   bool pack_w;       // the weight goes through an aligned, padded copy, piece by piece
   int64_t rows;      // tokens padded to kRowPad
