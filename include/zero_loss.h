@@ -30,8 +30,8 @@
  * Arithmetic: products of the given types' values with fp32 sums on the matrix
  * units; softmax statistics, losses and the sum over the vocabulary of dhidden
  * in fp32. g is rounded once to the given type for its products (bf16; fp16
- * after a power-of-two scaling that keeps the largest |u_t| near 2^15, undone
- * in fp32 before the result is rounded). In fp32 hidden, weight and g are each
+ * after a scaling that keeps the largest |u_t| near 2^14, undone in fp32 before
+ * the result is rounded). In fp32 hidden, weight and g are each
  * held as two fp16 parts under a power-of-two scale of their own, and three of
  * the four part products are summed: 24 bits for values above 2^-17 of the
  * tensor's largest magnitude (for g: of the largest |u_t|), an absolute 2^-40 of

@@ -11,7 +11,7 @@ dz = (N D + 16) e sum|h||W|, N = 3 or 1, and 2^-40 (max|h| sum|W| + max|W| sum|h
 for fp32. The log-sum-exp moves by at most the largest dz of the row plus the
 roundings of its own sums, (V/64 + 64 + 40) e relative in the sum and a few e of
 its value. One term of the logits' gradient is then off by |a| p (dz + dlse + 40 e)
-before it is rounded once (u; in fp16 and in fp32's fp16 parts at least 2^-39 of
+before it is rounded once (u; in fp16 and in fp32's fp16 parts at least 2^-38 of
 the largest upstream gradient, where the scaled form turns subnormal), and the
 products over it add (N K + 16) e sum|g||x|, in fp32 also 2^-40 of the largest
 |x| times sum|g|, before the result is rounded once more (u, and in fp16 2^-25
@@ -108,7 +108,7 @@ def reference(c, smoothing=0.0, z_loss=0.0, temperature=1.0, ignore_index=-100):
         dloss = dloss + smoothing * (V / 64 + 80) * E * z.abs().mean(1)
     dp = a.abs()[:, None] * p * (dz + dlse[:, None] + 40 * E) \
         + 8 * E * (a.abs()[:, None] * (p + want) + up.abs()[:, None] * want)
-    floor = up.abs().max() * tau * 2.0 ** -39 if dt != torch.bfloat16 and T else 0.0
+    floor = up.abs().max() * tau * 2.0 ** -38 if dt != torch.bfloat16 and T else 0.0
     dg = dp + u * g.abs() * (3.0 if f32 else 1.0) + floor
     dg = torch.where(live[:, None], dg, 0.0)
     ga = g.abs()

@@ -38,7 +38,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 // What the scan leaves for the kernels after it.
 struct Head {
   int live;         // rows that take part
-  float scale;      // power of two that g is held at
+  float scale;      // what g is held at
   float inv_scale;
   // fp32: the bits of the largest magnitude in the live rows of hidden, and in the
   // weight. (Non-negative floats order as their bits do, NaN above all.)
@@ -173,19 +173,23 @@ __global__ void __launch_bounds__(256) classify_kernel(Call c, uint8_t* state) {
   if (lane == 0) state[t] = bad ? 2 : any ? 1 : 0;
 }
 
-// One block numbers the live rows in order, and for the gradient finds the
-// power of two that brings the largest |g| a row can have to [2^14, 2^15):
-// inside fp16's range with 29 bits below it that are not subnormal.
+// One block numbers the live rows in order, and for the gradient finds the scale
+// that g is held at. The largest |g| a row can have comes to (2^13, 2^15], inside
+// fp16's range with 27 bits below it that are not subnormal; and of the factors
+// that do so, the one that makes the largest row's pull on its target a power of
+// two: with one upstream gradient for all rows, as a mean has, the -1 of every
+// row the model is unsure of is then exact, in place of all of them being rounded
+// the same way.
 __global__ void __launch_bounds__(1024) scan_kernel(Call c) {
   Head* head = reinterpret_cast<Head*>(c.ws + c.plan.o_head);
   int* rowmap = reinterpret_cast<int*>(c.ws + c.plan.o_rowmap);
   int* pos = reinterpret_cast<int*>(c.ws + c.plan.o_pos);
   const uint8_t* state = reinterpret_cast<const uint8_t*>(c.ws + c.plan.o_state);
   __shared__ int counts[16];
-  __shared__ float tops[16];
+  __shared__ float tops[16], pulls[16];
   const int tid = threadIdx.x, wave = tid / 64, lane = tid % 64;
   int base = 0;
-  float top = 0.0f;
+  float top = 0.0f, pull = 0.0f;
   for (int64_t t0 = 0; t0 < c.plan.tokens; t0 += 1024) {
     const int64_t t = t0 + tid;
     int st = 0;
@@ -212,9 +216,11 @@ __global__ void __launch_bounds__(1024) scan_kernel(Call c) {
         rowmap[at] = (int)t;
         pos[t] = at;
         if (c.plan.grad) {
-          float u = fabsf(c.upstream[t * c.upstream_stride]) * c.temperature;
-          if (c.z_loss != 0.0f) u *= 1.0f + 2.0f * c.z_loss * fabsf(c.lse_in[t]);
-          top = fmaxf(top, u);
+          const float u = fabsf(c.upstream[t * c.upstream_stride]) * c.temperature;
+          pull = fmaxf(pull, u);
+          top = fmaxf(top, c.z_loss != 0.0f
+                               ? u * (1.0f + 2.0f * c.z_loss * fabsf(c.lse_in[t]))
+                               : u);
         }
       } else {
         pos[t] = st == 0 ? -1 : -2;
@@ -223,48 +229,65 @@ __global__ void __launch_bounds__(1024) scan_kernel(Call c) {
     base += total;
   }
   top = wave_max(top);
-  if (lane == 0) tops[wave] = top;
+  pull = wave_max(pull);
+  if (lane == 0) {
+    tops[wave] = top;
+    pulls[wave] = pull;
+  }
   __syncthreads();
   if (tid == 0) {
-    for (int w = 0; w < 16; ++w) top = fmaxf(top, tops[w]);
+    for (int w = 0; w < 16; ++w) {
+      top = fmaxf(top, tops[w]);
+      pull = fmaxf(pull, pulls[w]);
+    }
     const int e = scale_exponent(top);
+    // pull (1 - smoothing) = part 2^q: dividing by the part, in [1, 2), leaves 2^q
+    pull *= 1.0f - c.smoothing;
+    const float part =
+        pull > 0x1p-80f && pull < 0x1p80f ? scalbnf(pull, -ilogbf(pull)) : 1.0f;
     head->live = base;
-    head->scale = ldexpf(1.0f, e);
-    head->inv_scale = ldexpf(1.0f, -e);
+    head->scale = ldexpf(1.0f, e) / part;
+    head->inv_scale = ldexpf(part, -e);
     head->top_h = head->top_w = 0;
   }
 }
 
 // ---- Packing --------------------------------------------------------------
-// fp32: the largest magnitudes of the live rows of hidden (blocks from `first_h`
-// on) and of the weight, 16 rows a block. Largest of largest in any order is the
-// same number, so the atomics leave nothing to chance.
-__global__ void __launch_bounds__(256) top_kernel(Call c, int first_h, bool wide_h, bool wide_w) {
+// fp32: the largest magnitudes of the weight and, in the last kTopHidden blocks,
+// of the live rows of hidden. The largest of largest in any order is the same
+// number, so the atomics leave nothing to chance; there is one a block, since
+// they all wait for each other (one a wave: 165 us in place of 40 for 154 MB).
+constexpr int kTopHidden = 64, kTopBlocks = 1024;
+__global__ void __launch_bounds__(256) top_kernel(Call c, bool wide_h, bool wide_w) {
   const Plan& p = c.plan;
   Head* head = reinterpret_cast<Head*>(c.ws + p.o_head);
-  const bool is_h = (int)blockIdx.x >= first_h;
-  const int64_t r0 = (int64_t)(is_h ? blockIdx.x - first_h : blockIdx.x) * 16;
-  const int64_t rows = is_h ? head->live : p.vocab;
+  const int first_h = (int)gridDim.x - kTopHidden;
+  const bool is_h = (int)blockIdx.x >= first_h, wide = is_h ? wide_h : wide_w;
+  const int64_t rows = is_h ? head->live : p.vocab, pitch = is_h ? c.hidden_stride : c.weight_stride;
   const int wave = threadIdx.x / 64, lane = threadIdx.x % 64;
+  const int64_t first = ((int)blockIdx.x - (is_h ? first_h : 0)) * 4 + wave;
+  const int64_t step = (is_h ? kTopHidden : first_h) * 4;
   uint32_t top = 0;
-  for (int64_t r = r0 + wave; r < min(rows, r0 + 16); r += 4) {
+  for (int64_t r = first; r < rows; r += step) {
     const int64_t row = is_h ? reinterpret_cast<const int*>(c.ws + p.o_rowmap)[r] : r;
-    const uint32_t* x = static_cast<const uint32_t*>(is_h ? c.hidden : c.weight) +
-                        row * (is_h ? c.hidden_stride : c.weight_stride);
-    int k = 0;
-    if (is_h ? wide_h : wide_w) {
-      for (k = lane * 4; k + 4 <= p.dim; k += 256) {
-        const u32x4 v = *reinterpret_cast<const u32x4*>(x + k);
+    const uint32_t* x = static_cast<const uint32_t*>(is_h ? c.hidden : c.weight) + row * pitch;
+    const int bulk = wide ? (int)p.dim / 4 * 4 : 0;
+    for (int k = lane * 4; k < bulk; k += 256) {
+      const u32x4 v = *reinterpret_cast<const u32x4*>(x + k);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) top = max(top, v[i] & 0x7fffffffu);
-      }
-      k = (int)p.dim / 4 * 4;
+      for (int i = 0; i < 4; ++i) top = max(top, v[i] & 0x7fffffffu);
     }
-    for (k += lane; k < p.dim; k += 64) top = max(top, x[k] & 0x7fffffffu);
+    for (int k = bulk + lane; k < p.dim; k += 64) top = max(top, x[k] & 0x7fffffffu);
   }
 #pragma unroll
   for (int d = 32; d; d >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
-  if (lane == 0 && top != 0) atomicMax(is_h ? &head->top_h : &head->top_w, top);
+  __shared__ uint32_t tops[4];
+  if (lane == 0) tops[wave] = top;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    top = max(max(tops[0], tops[1]), max(tops[2], tops[3]));
+    if (top != 0) atomicMax(is_h ? &head->top_h : &head->top_w, top);
+  }
 }
 
 // Eight elements from column k of a row, zero beyond `dim`, as 16-bit parts.
@@ -1074,9 +1097,10 @@ void rows_and_hidden(const Call& c, hipStream_t st) {
         c, reinterpret_cast<uint8_t*>(c.ws + p.o_state));
   scan_kernel<<<1, 1024, 0, st>>>(c);
   if (DT == kF32) {
-    const int first_h = (int)((p.vocab + 15) / 16);
-    top_kernel<<<(unsigned)(first_h + (p.tokens + 15) / 16), 256, 0, st>>>(
-        c, first_h, rows_aligned(c.hidden, c.hidden_stride, p.dtype, 4),
+    const int64_t w_blocks = (p.vocab + 3) / 4;
+    const int blocks = (int)(w_blocks < kTopBlocks ? w_blocks : kTopBlocks) + kTopHidden;
+    top_kernel<<<blocks, 256, 0, st>>>(
+        c, rows_aligned(c.hidden, c.hidden_stride, p.dtype, 4),
         rows_aligned(c.weight, c.weight_stride, p.dtype, 4));
   }
   if (p.tokens > 0)
