@@ -634,8 +634,10 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, 2) product_kernel(Product
     }
     half(fa0, fb0, it & 1, 1, fa1, fb1, No{}, 0);
     half(fa1, fb1, -1, 0, fa0, fb0, No{}, 0);
+    if constexpr (Epi::kTurns) meet();
   }
-  epi.template tile<MI, NJ>(m0 + wm, n0 + wn, n_ext, split, acc);
+  epi.template tile<MI, NJ>(m0 + wm, n0 + wn, n_ext, split, acc,
+                            lds + wave * 4096);
 }
 
 // ---- What happens to a tile -------------------------------------------------
@@ -645,6 +647,29 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, 2) product_kernel(Product
 // Forward: the tile's rows m are vocabulary, its columns n live rows. Each wave
 // leaves the largest logit, the sum of exponentials and the sum of logits of
 // its stretch of the vocabulary.
+// Sixteen columns of 128 results, four 16-bit values in a register pair (`part`,
+// one for each square), become rows of 256 bytes through 4 KB of LDS that are the
+// wave's own once the stages are done with: then a store has 16 bytes a lane and four whole rows, in place of 8 bytes
+// and sixteen pieces of 32. put(row, group, value) gets the rows' 16-byte groups.
+// Groups are exchanged by their row, so that neither side meets a bank twice.
+template <class Put>
+__device__ __forceinline__ void turn_rows(lds_char* turn, const u32x2 (&part)[8], Put put) {
+  const int lane = threadIdx.x % 64, r = lane % 16, g = lane / 16;
+  typedef __attribute__((address_space(3))) u32x2 lds_u32x2;
+  typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    *reinterpret_cast<lds_u32x2*>(turn + r * 256 + ((i * 2 + g / 2) ^ r) * 16 + g % 2 * 8) =
+        part[i];
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int row = q * 4 + g;
+    put(row, r, *reinterpret_cast<lds_u32x4*>(turn + row * 256 + (r ^ row) * 16));
+  }
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+}
+
 template <int DT>
 struct StatEpi {
   const Head* head;
@@ -654,26 +679,45 @@ struct StatEpi {
   float inv_temp;
   int m_base;       // vocabulary index of m = 0
   int vocab;
+  static constexpr bool kTurns = false;
   template <int MI, int NJ>
-  __device__ __forceinline__ void tile(int m0, int n0, int n_ext, int, f32x4 (&acc)[MI][NJ]) {
+  __device__ __forceinline__ void tile(int m0, int n0, int n_ext, int, f32x4 (&acc)[MI][NJ],
+                                       lds_char*) {
     static_assert(MI * 16 == kStatRows, "one partial per wave");
     const int lane = threadIdx.x % 64;
     const int m_hi = vocab - m_base;
-    if (m0 >= round_up_int(m_hi, (int)kStatRows)) return;
+    if (m0 >= round_up_int(m_hi, (int)kStatRows) || n0 >= n_ext) return;
     const float uh = undo_h<DT>(head), uw = undo_w<DT>(head);
+    const bool edge = m0 + (int)kStatRows > m_hi;  // some of it is beyond the vocabulary
+    // The sums of exponentials are this kernel's second cost after the products (an
+    // exponential takes four times an addition), so what only some tiles need is
+    // kept out of the others' way.
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
       float top = -INFINITY, total = 0.0f, plain = 0.0f;
 #pragma unroll
       for (int i = 0; i < MI; ++i)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const bool in = m0 + i * 16 + lane / 16 * 4 + r < m_hi;
-          const float z = in ? logit_of<DT>(acc[i][j][r], uh, uw, inv_temp) : -INFINITY;
-          acc[i][j][r] = z;
-          plain += in ? z : 0.0f;
-          top = fmaxf(top, z);
-        }
+        for (int r = 0; r < 4; ++r) acc[i][j][r] = logit_of<DT>(acc[i][j][r], uh, uw, inv_temp);
+      if (sum != nullptr) {
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            plain += m0 + i * 16 + lane / 16 * 4 + r < m_hi ? acc[i][j][r] : 0.0f;
+      }
+      if (edge) {
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (m0 + i * 16 + lane / 16 * 4 + r >= m_hi) acc[i][j][r] = -INFINITY;
+      }
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        top = fmaxf(fmaxf(top, acc[i][j][0]), acc[i][j][1]);
+        top = fmaxf(fmaxf(top, acc[i][j][2]), acc[i][j][3]);
+      }
       top = fmaxf(top, __shfl_xor(top, 16));
       top = fmaxf(top, __shfl_xor(top, 32));
       const float from = top == -INFINITY ? 0.0f : top;  // -inf - -inf would be NaN
@@ -683,14 +727,14 @@ struct StatEpi {
         for (int r = 0; r < 4; ++r) total += exp_f(acc[i][j][r] - from);
       total += __shfl_xor(total, 16);
       total += __shfl_xor(total, 32);
-      plain += __shfl_xor(plain, 16);
-      plain += __shfl_xor(plain, 32);
       const int n = n0 + j * 16 + lane % 16;
-      if (lane < 16 && n < n_ext) {
-        const int64_t at = n * cols + (m_base + m0) / kStatRows;
-        stat[at] = make_float2(top, total);
-        if (sum != nullptr) sum[at] = plain;
+      const int64_t at = n * cols + (m_base + m0) / kStatRows;
+      if (sum != nullptr) {
+        plain += __shfl_xor(plain, 16);
+        plain += __shfl_xor(plain, 32);
+        if (lane < 16 && n < n_ext) sum[at] = plain;
       }
+      if (lane < 16 && n < n_ext) stat[at] = make_float2(top, total);
     }
   }
 };
@@ -707,25 +751,51 @@ struct GradEpi {
   int64_t plane, ld;
   float inv_temp;
   int m_base, m_ext;   // first vocabulary index, how many of it are real
+  bool shift;          // rows have a constant to take off (label smoothing)
+  static constexpr bool kTurns = true;
   template <int MI, int NJ>
-  __device__ __forceinline__ void tile(int m0, int n0, int n_ext, int, f32x4 (&acc)[MI][NJ]) {
+  __device__ __forceinline__ void tile(int m0, int n0, int n_ext, int, f32x4 (&acc)[MI][NJ],
+                                       lds_char* turn) {
+    constexpr int kPlanes = DT == kF32 ? kParts : 1;
     const int lane = threadIdx.x % 64;
     const float uh = undo_h<DT>(head), uw = undo_w<DT>(head);
+    const bool edge = m0 + MI * 16 > m_ext || n0 + NJ * 16 > n_ext;
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
       const int n = n0 + j * 16 + lane % 16;
       const RowParam rp = rows[n];
-      const bool real = n < n_ext;
-      const int at = rp.target - m_base;
+      const int at = rp.target - m_base - m0 - lane / 16 * 4;  // 16 i + r where it is this lane's
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          acc[i][j][r] =
+              rp.a * exp_f(logit_of<DT>(acc[i][j][r], uh, uw, inv_temp) - rp.lse);
+      if (shift) {
+#pragma unroll
+        for (int i = 0; i < MI; ++i) acc[i][j] -= rp.c;
+      }
+      if (__any(at >= 0 && at < MI * 16 && (at & 15) < 4)) {  // one row's target in 128: rare
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (at == i * 16 + r) acc[i][j][r] -= rp.hit;
+      }
+      if (edge) {
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (n >= n_ext || m0 + i * 16 + lane / 16 * 4 + r >= m_ext) acc[i][j][r] = 0.0f;
+      }
+      u32x2 packed[kPlanes][MI];
 #pragma unroll
       for (int i = 0; i < MI; ++i) {
-        const int m = m0 + i * 16 + lane / 16 * 4;
-        u16 parts[kParts][4];
+        u16 parts[kPlanes][4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          float x = rp.a * exp_f(logit_of<DT>(acc[i][j][r], uh, uw, inv_temp) - rp.lse) - rp.c;
-          if (m + r == at) x -= rp.hit;
-          x = real && m + r < m_ext ? x : 0.0f;
+          const float x = acc[i][j][r];
           if constexpr (DT == kF32) {
             u16 p[kParts];
             split2(x, p);
@@ -734,14 +804,16 @@ struct GradEpi {
             parts[0][r] = DT == kBF16 ? bf16_bits(x) : f16_bits(x);
           }
         }
-        if (m < ld) {
 #pragma unroll
-          for (int s = 0; s < (DT == kF32 ? kParts : 1); ++s)
-            *reinterpret_cast<u32x2*>(g + s * plane + n * ld + m) =
-                u32x2{parts[s][0] | (uint32_t)parts[s][1] << 16,
-                      parts[s][2] | (uint32_t)parts[s][3] << 16};
-        }
+        for (int s = 0; s < kPlanes; ++s)
+          packed[s][i] = u32x2{parts[s][0] | (uint32_t)parts[s][1] << 16,
+                               parts[s][2] | (uint32_t)parts[s][3] << 16};
       }
+#pragma unroll
+      for (int s = 0; s < kPlanes; ++s)
+        turn_rows(turn, packed[s], [&](int row, int group, u32x4 v) {
+          *reinterpret_cast<u32x4*>(g + s * plane + (n0 + j * 16 + row) * ld + m0 + group * 8) = v;
+        });
     }
   }
 };
@@ -753,9 +825,10 @@ struct SumEpi {
   int64_t slab, ld;
   int m_ext;
   bool add;
+  static constexpr bool kTurns = false;
   template <int MI, int NJ>
   __device__ __forceinline__ void tile(int m0, int n0, int n_ext, int split,
-                                       f32x4 (&acc)[MI][NJ]) {
+                                       f32x4 (&acc)[MI][NJ], lds_char*) {
     const int lane = threadIdx.x % 64;
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
@@ -779,14 +852,42 @@ struct WeightEpi {
   int64_t ld;
   int64_t v0;
   int m_ext;
-  bool wide;       // rows start at multiples of four elements' size
+  int wide;        // rows start at multiples of this many elements' size: 8, 4 or 1
   const Head* head;
+  static constexpr bool kTurns = DT != kF32;
   template <int MI, int NJ>
-  __device__ __forceinline__ void tile(int m0, int n0, int n_ext, int, f32x4 (&acc)[MI][NJ]) {
+  __device__ __forceinline__ void tile(int m0, int n0, int n_ext, int, f32x4 (&acc)[MI][NJ],
+                                       lds_char* turn) {
     const int lane = threadIdx.x % 64;
     const float s = head->inv_scale, uh = undo_h<DT>(head);
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
+      if constexpr (DT != kF32) {
+        if (wide == 8) {
+          u32x2 packed[MI];
+#pragma unroll
+          for (int i = 0; i < MI; ++i) {
+            const f32x4 x = acc[i][j] * uh * s;
+            u16 b[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) b[r] = DT == kBF16 ? bf16_bits(x[r]) : f16_bits(x[r]);
+            packed[i] = u32x2{b[0] | (uint32_t)b[1] << 16, b[2] | (uint32_t)b[3] << 16};
+          }
+          turn_rows(turn, packed, [&](int row, int group, u32x4 v) {
+            const int n = n0 + j * 16 + row, m = m0 + group * 8;
+            if (n >= n_ext) return;
+            u16* to = static_cast<u16*>(out) + (v0 + n) * ld + m;
+            if (m + 8 <= m_ext) {
+              *reinterpret_cast<u32x4*>(to) = v;
+            } else {
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                if (m + e < m_ext) to[e] = (u16)(v[e / 2] >> (16 * (e % 2)));
+            }
+          });
+          continue;
+        }
+      }
       const int n = n0 + j * 16 + lane % 16;
       if (n >= n_ext) continue;
 #pragma unroll
@@ -794,7 +895,7 @@ struct WeightEpi {
         const int m = m0 + i * 16 + lane / 16 * 4;
         const f32x4 x = acc[i][j] * uh * s;
         if (m + 4 <= m_ext) {
-          store4<DT>(out, (v0 + n) * ld + m, x, wide);
+          store4<DT>(out, (v0 + n) * ld + m, x, wide >= 4);
         } else {
 #pragma unroll
           for (int r = 0; r < 4; ++r)
@@ -1174,7 +1275,7 @@ void grad_type(const Call& c, hipStream_t st) {
     // g of the piece
     Product g = logits_product<DT>(c, w, ldw, real);
     GradEpi<DT> ge{head, reinterpret_cast<const RowParam*>(c.ws + p.o_rowp), gbuf, p.rows * p.piece,
-                   p.piece, 1.0f / c.temperature, (int)v0, (int)real};
+                   p.piece, 1.0f / c.temperature, (int)v0, (int)real, c.smoothing != 0.0f};
     product<DT, false, false>(g, ge, st);
     if (c.k > 0 && p.tokens > 0) entry_kernel<DT><<<(unsigned)p.tokens, 64, 0, st>>>(c, v0);
     // dhidden += g W: the inner index is the piece's vocabulary
@@ -1207,7 +1308,10 @@ void grad_type(const Call& c, hipStream_t st) {
       d.splits = 1;
       d.head = head;
       WeightEpi<DT> we{c.dweight, c.dweight_stride, v0, (int)p.dim,
-                       rows_aligned(c.dweight, c.dweight_stride, p.dtype, 4), head};
+                       rows_aligned(c.dweight, c.dweight_stride, p.dtype, 8)   ? 8
+                       : rows_aligned(c.dweight, c.dweight_stride, p.dtype, 4) ? 4
+                                                                               : 1,
+                       head};
       product<DT, true, true>(d, we, st);
     }
   }
