@@ -38,6 +38,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 // What the scan leaves for the kernels after it.
 struct Head {
   int live;         // rows that take part
+  int splits;       // runs that dhidden's sum over a piece of the vocabulary is cut into
   float scale;      // what g is held at
   float inv_scale;
   // fp32: the bits of the largest magnitude in the live rows of hidden, and in the
@@ -173,6 +174,23 @@ __global__ void __launch_bounds__(256) classify_kernel(Call c, uint8_t* state) {
   if (lane == 0) state[t] = bad ? 2 : any ? 1 : 0;
 }
 
+// dhidden has few tiles, [live, dim], and a long sum, over the piece's vocabulary:
+// the sum is cut into as many runs as make the rounds of 256 tiles that the chip
+// holds at once end soonest, a round taking the run's steps and about four more.
+// Lane l of the wave looks at l + 1 runs.
+__device__ __forceinline__ int choose_splits(const Plan& p, int live) {
+  const int lane = threadIdx.x % 64, s = lane + 1;
+  const int bn = p.tokens <= 64 ? 64 : 256, held = p.tokens <= 64 ? 512 : 256;
+  const int tiles = (live + bn - 1) / bn * (int)((p.dimp + 255) / 256);
+  const int steps = ((int)(p.piece / 64) + s - 1) / s;
+  int cost = (tiles * s + held - 1) / held * (steps + 4);
+  if (s > 1 && (tiles * s > p.acc_tiles || steps < 4)) cost = 0x7fffffff;
+  int best = cost;
+#pragma unroll
+  for (int d = 32; d; d >>= 1) best = min(best, __shfl_xor(best, d));
+  return __builtin_ctzll(__ballot(cost == best)) + 1;
+}
+
 // One block numbers the live rows in order, and for the gradient finds the scale
 // that g is held at. The largest |g| a row can have comes to (2^13, 2^15], inside
 // fp16's range with 27 bits below it that are not subnormal; and of the factors
@@ -228,6 +246,7 @@ __global__ void __launch_bounds__(1024) scan_kernel(Call c) {
     }
     base += total;
   }
+  const int splits = c.plan.grad && wave == 0 ? choose_splits(c.plan, base) : 1;
   top = wave_max(top);
   pull = wave_max(pull);
   if (lane == 0) {
@@ -246,6 +265,7 @@ __global__ void __launch_bounds__(1024) scan_kernel(Call c) {
     const float part =
         pull > 0x1p-80f && pull < 0x1p80f ? scalbnf(pull, -ilogbf(pull)) : 1.0f;
     head->live = base;
+    head->splits = splits;
     head->scale = ldexpf(1.0f, e) / part;
     head->inv_scale = ldexpf(part, -e);
     head->top_h = head->top_w = 0;
@@ -402,8 +422,8 @@ struct Product {
   int n_real;      // columns that mean something
   int inner;       // inner extent, a multiple of 64 (the most there can be, where live_inner)
   bool live_n, live_inner;  // the extent is the live count, rounded up to 64 for the inner one
+  bool split;      // the inner extent is cut into head->splits runs
   int segs;        // 1, or kSegs part products
-  int splits;      // the inner extent in this many runs
   const Head* head;
 };
 
@@ -496,7 +516,8 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, 2) product_kernel(Product
   // dies (blocks go to them in turn) gets a run of them, so that the tiles in
   // flight on a die share rows and columns in its cache.
   const int mt = (g.m + 255) / 256, nt = (n_ext + BN - 1) / BN;
-  const int total = mt * nt * g.splits, run = (total + 7) / 8;
+  const int splits = g.split ? g.head->splits : 1;
+  const int total = mt * nt * splits, run = (total + 7) / 8;
   int id = (int)blockIdx.x;
   if (id / 8 >= run) return;
   id = (id % 8) * run + id / 8;
@@ -507,7 +528,7 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, 2) product_kernel(Product
   id -= strip * 4 * mt;
   const int m0 = id / wide * 256, n0 = (strip * 4 + id % wide) * BN;
 
-  const int chunk = round_up_int((inner + g.splits - 1) / g.splits, 64);
+  const int chunk = round_up_int((inner + splits - 1) / splits, 64);
   const int k_lo = min(inner, split * chunk), k_hi = min(inner, k_lo + chunk);
   const int steps = (k_hi - k_lo) / 64, all = steps * g.segs;
   const int tid = threadIdx.x, lane = tid % 64;
@@ -609,7 +630,17 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, 2) product_kernel(Product
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
   };
-  if (all > 0) {
+  if (all > 0 && n0 + wn >= n_ext) {
+    // no column of this wave's is real: it copies its share and keeps step
+    copy(0);
+    meet();
+    if (all > 1) copy(1);
+    for (int it = 0; it + 1 < all; ++it) {
+      meet();
+      if (it + 2 < all) copy(it & 1);
+    }
+    if constexpr (Epi::kTurns) meet();
+  } else if (all > 0) {
     // Each half step's operands are read while the half before is multiplied, and
     // the block meets between them: there the second half is in registers, so the
     // stage may be copied over, and the matrix units have work on both sides.
@@ -818,11 +849,11 @@ struct GradEpi {
   }
 };
 
-// dhidden's sum over the vocabulary: fp32 [splits][rows][ld], added to from the
+// dhidden's sum over the vocabulary: fp32 [splits][live][ld], added to from the
 // second piece on. Rows m are hidden's columns, columns n live rows.
 struct SumEpi {
   float* acc_out;
-  int64_t slab, ld;
+  int64_t ld;
   int m_ext;
   bool add;
   static constexpr bool kTurns = false;
@@ -838,7 +869,7 @@ struct SumEpi {
       for (int i = 0; i < MI; ++i) {
         const int m = m0 + i * 16 + lane / 16 * 4;
         if (m >= m_ext) continue;
-        f32x4* o = reinterpret_cast<f32x4*>(acc_out + split * slab + n * ld + m);
+        f32x4* o = reinterpret_cast<f32x4*>(acc_out + ((int64_t)split * n_ext + n) * ld + m);
         *o = add ? *o + acc[i][j] : acc[i][j];
       }
     }
@@ -1144,14 +1175,16 @@ __global__ void __launch_bounds__(64) dhidden_kernel(Call c, bool wide) {
   f32x4 x = {};
   if (at >= 0) {
     const float* acc = reinterpret_cast<const float*>(c.ws + p.o_acc) + (int64_t)at * p.dimp + k;
-    for (int q = 0; q < p.splits; q += 8) {
+    const int splits = head->splits;
+    const int64_t slab = (int64_t)head->live * p.dimp;
+    for (int q = 0; q < splits; q += 8) {
       f32x4 v[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        v[i] = *reinterpret_cast<const f32x4*>(acc + min(q + i, p.splits - 1) * p.rows * p.dimp);
+        v[i] = *reinterpret_cast<const f32x4*>(acc + min(q + i, splits - 1) * slab);
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (q + i < p.splits) x += v[i];
+        if (q + i < splits) x += v[i];
     }
     x = x * undo_w<DT>(head) * head->inv_scale;
   }
@@ -1174,8 +1207,9 @@ bool rows_aligned(const void* p, int64_t stride, int dt, int n) {
 }
 
 template <int DT, bool TA, bool TB, int BN, class Epi>
-void product_tiles(const Product& g, const Epi& epi, hipStream_t st) {
-  const int64_t total = (int64_t)((g.m + 255) / 256) * ((g.n + BN - 1) / BN) * g.splits;
+void product_tiles(const Product& g, const Epi& epi, int64_t most_split, hipStream_t st) {
+  int64_t total = (int64_t)((g.m + 255) / 256) * ((g.n + BN - 1) / BN);
+  if (g.split && total < most_split) total = most_split;
   product_kernel<DT, TA, TB, BN, Epi>
       <<<(unsigned)((total + 7) / 8 * 8), Shape<BN>::kThreads, 0, st>>>(g, epi);
 }
@@ -1183,11 +1217,11 @@ void product_tiles(const Product& g, const Epi& epi, hipStream_t st) {
 // Columns are tokens (few of them take narrower tiles) or, where the right
 // operand is transposed, vocabulary.
 template <int DT, bool TA, bool TB, class Epi>
-void product(const Product& g, const Epi& epi, hipStream_t st) {
+void product(const Product& g, const Epi& epi, hipStream_t st, int64_t most_split = 0) {
   if constexpr (!TB) {
-    if (g.n_real <= 64) return product_tiles<DT, TA, TB, 64, Epi>(g, epi, st);
+    if (g.n_real <= 64) return product_tiles<DT, TA, TB, 64, Epi>(g, epi, most_split, st);
   }
-  product_tiles<DT, TA, TB, 256, Epi>(g, epi, st);
+  product_tiles<DT, TA, TB, 256, Epi>(g, epi, most_split, st);
 }
 
 template <int DT>
@@ -1236,7 +1270,6 @@ Product logits_product(const Call& c, const u16* w, int64_t ldw, int64_t real) {
   g.inner = (int)p.dimp;
   g.live_n = true;
   g.segs = DT == kF32 ? kSegs : 1;
-  g.splits = 1;
   g.head = reinterpret_cast<const Head*>(c.ws + p.o_head);
   return g;
 }
@@ -1289,11 +1322,11 @@ void grad_type(const Call& c, hipStream_t st) {
       d.inner = round_up_int((int)real, 64);
       d.live_n = true;
       d.segs = g.segs;
-      d.splits = p.splits;
+      d.split = true;
       d.head = head;
-      SumEpi se{reinterpret_cast<float*>(c.ws + p.o_acc), p.rows * p.dimp, p.dimp, (int)p.dimp,
+      SumEpi se{reinterpret_cast<float*>(c.ws + p.o_acc), p.dimp, (int)p.dimp,
                 v0 > 0};
-      product<DT, true, false>(d, se, st);
+      product<DT, true, false>(d, se, st, p.acc_tiles);
     }
     // dweight of the piece: the inner index is the live rows
     if (c.dweight != nullptr) {
@@ -1305,7 +1338,6 @@ void grad_type(const Call& c, hipStream_t st) {
       d.inner = (int)p.rows;
       d.live_inner = true;
       d.segs = g.segs;
-      d.splits = 1;
       d.head = head;
       WeightEpi<DT> we{c.dweight, c.dweight_stride, v0, (int)p.dim,
                        rows_aligned(c.dweight, c.dweight_stride, p.dtype, 8)   ? 8

@@ -80,6 +80,35 @@ zero_status check_head(const zero_head* h) {
   return ZERO_OK;
 }
 
+// Vocabulary rows per piece. The largest allowed has 256 MiB of g (what the chip's
+// last cache holds), or of packed weights. Smaller ones are taken where the rounds
+// of 256 tiles that the chip holds at once come out fuller, in all: the logits'
+// tiles [piece, tokens] take dim / 64 steps each, dweight's [dim, piece] tokens / 64,
+// either about four steps more, and a piece about eight in launches.
+int64_t choose_piece(const zloss::Plan& p, int64_t whole) {
+  constexpr int64_t kPieceBytes = INT64_C(256) << 20;
+  int64_t most = std::min<int64_t>(whole, INT64_C(1) << 21);
+  if (p.grad) most = std::min(most, kPieceBytes / (p.rows * 2 * p.planes));
+  if (p.pack_w) most = std::min(most, kPieceBytes / (p.dimp * 2 * p.planes));
+  most = std::max<int64_t>(most / zloss::kVocPad * zloss::kVocPad, std::min<int64_t>(whole, 2048));
+  const int64_t least = ceil_div(whole, most);
+  int64_t best = most, best_cost = INT64_MAX;
+  for (int64_t n = least; n <= least + 8; ++n) {
+    const int64_t piece = round_up(ceil_div(p.vocab, n), zloss::kVocPad);
+    int64_t cost = 0;
+    for (int64_t v0 = 0; v0 < p.vocab; v0 += piece) {
+      const int64_t m = ceil_div(std::min(piece, p.vocab - v0), 256);
+      cost += 8 + ceil_div(m * (p.rows / 256), 256) * (p.dimp / 64 + 4);
+      if (p.grad) cost += ceil_div(m * ceil_div(p.dimp, 256), 256) * (p.rows / 64 + 4);
+    }
+    if (cost < best_cost) {
+      best = piece;
+      best_cost = cost;
+    }
+  }
+  return best;
+}
+
 // The pieces and the workspace of one call.
 zloss::Plan make_plan(const zero_head& h, bool grad) {
   zloss::Plan p{};
@@ -95,22 +124,15 @@ zloss::Plan make_plan(const zero_head& h, bool grad) {
   // kDimPad; lane offsets within 256 rows are 32-bit.
   p.pack_w = p.planes > 1 || p.dimp != h.dim || h.weight_stride % 8 != 0 ||
              h.weight_stride > (INT64_C(1) << 22) || !aligned(h.weight, 16);
-  // Bytes per vocabulary row of a piece: its logits' gradient, its packed weights.
-  constexpr int64_t kPieceBytes = INT64_C(256) << 20;
   const int64_t whole = round_up(h.vocab, zloss::kVocPad);
-  int64_t piece = std::min<int64_t>(whole, INT64_C(1) << 21);
-  if (grad) piece = std::min(piece, kPieceBytes / (p.rows * 2 * p.planes));
-  if (p.pack_w) piece = std::min(piece, kPieceBytes / (p.dimp * 2 * p.planes));
-  piece = std::max<int64_t>(piece, std::min<int64_t>(whole, 2048));
-  if (!grad && !p.pack_w) piece = whole;  // nothing of a piece is stored
-  const int64_t n = ceil_div(h.vocab, std::max<int64_t>(piece / zloss::kVocPad, 1) * zloss::kVocPad);
-  p.piece = round_up(ceil_div(h.vocab, n), zloss::kVocPad);
+  p.piece = whole;  // the loss of unpacked weights stores nothing of a piece
+  if (grad || p.pack_w) p.piece = choose_piece(p, whole);
   p.stat_cols = whole / zloss::kStatRows;
-  // dhidden sums over the vocabulary: with few tiles of [tokens, dim] the sum
-  // is split so that there are tiles for the chip's 256 compute units.
-  const int64_t tiles = (p.rows / zloss::kRowPad) * ceil_div(p.dimp, 256);
-  p.splits = (int)std::max<int64_t>(
-      1, std::min<int64_t>({256 / tiles, 64, p.piece / 512}));
+  // dhidden's sum over the vocabulary may be cut into slabs, as long as they are
+  // at most this many tiles of 256 columns, and of 256 tokens or 64.
+  const int64_t tile_rows = h.tokens <= 64 ? 64 : 256;
+  const int64_t tiles = ceil_div(std::max<int64_t>(h.tokens, 1), tile_rows) * ceil_div(p.dimp, 256);
+  p.acc_tiles = (int)std::max<int64_t>(512, tiles);
 
   size_t at = 0;
   const auto take = [&at](int64_t bytes) {
@@ -131,7 +153,7 @@ zloss::Plan make_plan(const zero_head& h, bool grad) {
   } else {
     p.o_rowp = take(p.rows * 32);
     p.o_g = take(p.planes * p.rows * p.piece * 2);
-    p.o_acc = take((int64_t)p.splits * p.rows * p.dimp * 4);
+    p.o_acc = take(p.acc_tiles * tile_rows * 256 * 4);
   }
   p.total = at;
   return p;

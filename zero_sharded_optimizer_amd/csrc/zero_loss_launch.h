@@ -28,7 +28,7 @@ struct Plan {
   int64_t dimp;      // dim padded to kDimPad
   int64_t piece;     // vocabulary rows per piece, a multiple of kVocPad
   int64_t stat_cols; // softmax partials per token
-  int splits;        // slabs the vocabulary sum of dhidden is split over
+  int acc_tiles;     // tiles that the slabs of dhidden's sum have room for
   // workspace offsets, bytes
   size_t o_head;     // Head: live count, scale
   size_t o_rowmap;   // int32[rows]: live position -> token
@@ -41,7 +41,7 @@ struct Plan {
   size_t o_entry;    // float [tokens] (cross entropy, forward): the targets' logits
   size_t o_rowp;     // RowParam[rows] (gradient)
   size_t o_g;        // 16-bit [planes][rows][piece] (gradient)
-  size_t o_acc;      // float [splits][rows][dimp] (gradient)
+  size_t o_acc;      // float [splits][live rows][dimp] (gradient)
   size_t total;
 };
 
