@@ -448,6 +448,9 @@ struct Shape {
   static constexpr int kStage = (256 + BN) * 128;  // bytes
 };
 
+// The inner step that the logits' narrow tiles of vocabulary row m start at.
+__device__ __forceinline__ int first_step(int m, int steps) { return m / 256 * 5 % steps; }
+
 // Byte offsets, from the tile's corner (r0 < o.rows: a tile starts on a real row), that lane `l` of wave `w` copies from
 // with its i-th instruction of 64 groups.
 template <bool T, int R>
@@ -549,7 +552,14 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, 2) product_kernel(Product
   const int64_t step_a = TA ? g.a.ld * 128 : 128, step_b = TB ? g.b.ld * 128 : 128;
   const char* pa = corner(g.a, TA, m0, g.segs > 1 ? seg_a(0) : 0);
   const char* pb = corner(g.b, TB, n0, g.segs > 1 ? seg_b(0) : 0);
-  int seg = 0, at = 0;  // the next step to copy
+  // Few tokens: what counts is the weight's way from memory. Its rows are a power of
+  // two apart more often than not, and blocks that all read the same columns would
+  // ask the same channels: each row of tiles starts at another step and comes round.
+  constexpr bool kTurned = BN == 64 && !TA && !TB;
+  const int turn = kTurned && steps > 0 ? first_step(m0, steps) : 0;
+  int seg = 0, at = turn;  // the next step to copy
+  pa += turn * step_a;
+  pb += turn * step_b;
   // Instruction i of a step's copies, A's first.
   const auto copy_part = [&](int stage, int i) {
     const uint32_t to = lds_at + stage * S::kStage;
@@ -571,11 +581,16 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, 2) product_kernel(Product
   const auto after_copy = [&]() {
     pa += step_a;
     pb += step_b;
-    if (++at == steps) {
+    if (kTurned && ++at == steps) {
       at = 0;
+      pa -= steps * step_a;
+      pb -= steps * step_b;
+    }
+    if (kTurned ? at == turn : ++at == steps) {
+      if (!kTurned) at = 0;
       if (++seg < g.segs) {
-        pa = corner(g.a, TA, m0, seg_a(seg));
-        pb = corner(g.b, TB, n0, seg_b(seg));
+        pa = corner(g.a, TA, m0, seg_a(seg)) + turn * step_a;
+        pb = corner(g.b, TB, n0, seg_b(seg)) + turn * step_b;
         if constexpr (TA) {
 #pragma unroll
           for (int i = 0; i < kCopyA; ++i)
@@ -966,24 +981,25 @@ __global__ void __launch_bounds__(256) gather_kernel(Call c, const u16* w, int64
   const u16* h = reinterpret_cast<const u16*>(c.ws + p.o_h) +
                  (int64_t)min(row, live - 1) * p.dimp + lane / 16 * 8;
   const u16* a = w + (mine ? m : 0) * ldw + lane / 16 * 8;
+  // the narrow tiles' order of steps, each pair in that of its own weight row
+  const int turn = p.tokens <= 64 && mine ? first_step((int)m, (int)p.dimp / 64) * 64 : 0;
   f32x4 acc = {};
   for (int seg = 0; seg < (DT == kF32 ? kSegs : 1); ++seg) {
     const u16* pa = a + (DT == kF32 ? seg_a(seg) * p.piece * p.dimp : 0);
     const u16* pb = h + (DT == kF32 ? seg_b(seg) * p.rows * p.dimp : 0);
-    int k0 = 0;
-    for (; k0 + 256 <= p.dimp; k0 += 256) {  // eight loads on their way at a time
+    for (int k0 = 0; k0 < p.dimp; k0 += 256) {  // eight loads on their way at a time
       u32x4 va[8], vb[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        va[i] = *reinterpret_cast<const u32x4*>(pa + k0 + i * 32);
-        vb[i] = *reinterpret_cast<const u32x4*>(pb + k0 + i * 32);
+        int k = min(k0 + i * 32, (int)p.dimp - 32) + turn;
+        k -= k >= p.dimp ? (int)p.dimp : 0;
+        va[i] = *reinterpret_cast<const u32x4*>(pa + k);
+        vb[i] = *reinterpret_cast<const u32x4*>(pb + k);
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc = mfma<DT>(va[i], vb[i], acc);
+      for (int i = 0; i < 8; ++i)
+        if (k0 + i * 32 < p.dimp) acc = mfma<DT>(va[i], vb[i], acc);
     }
-    for (; k0 < p.dimp; k0 += 32)
-      acc = mfma<DT>(*reinterpret_cast<const u32x4*>(pa + k0),
-                     *reinterpret_cast<const u32x4*>(pb + k0), acc);
   }
   // lane l holds rows l / 16 * 4 + 0..3 of column l % 16
   if (mine && q / 4 == lane / 16) {
