@@ -40,7 +40,7 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 // Up to here the tiles are 64 columns wide.
 constexpr int kFewTokens = 64;
 
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // What the scan leaves for the kernels after it.
 struct Head {
@@ -64,11 +64,15 @@ __device__ __forceinline__ int scale_exponent(uint32_t bits) {
   return scale_exponent(__builtin_bit_cast(float, bits));
 }
 
-// Per live row, for the logits' gradient g = a exp(z - lse) - c - hit [j = target].
+// Per live row, for the logits' gradient
+//   g = a exp(z / temperature - lse) - c - hit [j = target]
+//     = a2 2^(z log2(e) / temperature - base) - c - ..
+// with base the lse over ln 2, rounded to sixteenths, and the rest of it in a2.
 struct RowParam {
-  float lse, a, c, hit;
+  float a2, base, c, hit;
   int target;       // global vocabulary index, or -1
-  int pad[3];
+  float a, lse;
+  int pad;
 };
 static_assert(sizeof(RowParam) == 32, "the plan counts 32 bytes a row");
 
@@ -140,6 +144,10 @@ __device__ __forceinline__ void store4(void* p, int64_t i, f32x4 x, bool wide) {
 // exp of x in fp32: the product with log2(e) is rounded once, the rest is the
 // hardware's exp2 (1 ulp).
 __device__ __forceinline__ float exp_f(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
+
+// The multiple of 1/16 next to x: exact in fp32 (as are differences of such), so
+// that an exponent of two relative to it is rounded once, by its own size.
+__device__ __forceinline__ float sixteenths(float x) { return rintf(x * 16.0f) * 0.0625f; }
 
 template <int DT>
 __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
@@ -236,6 +244,9 @@ __device__ __forceinline__ RowParam row_param(const Call& c, int64_t t, float sc
     rp.a = u * c.temperature;
     rp.target = -1;
   }
+  const double l2 = rp.lse * 1.4426950408889634;
+  rp.base = sixteenths((float)l2);
+  rp.a2 = (float)(rp.a * exp2(rp.base - l2));
   return rp;
 }
 
@@ -489,11 +500,17 @@ template <int DT>
 __device__ __forceinline__ float undo_w(const Head* head) {
   return DT == kF32 ? ldexpf(1.0f, -scale_exponent(head->top_w)) : 1.0f;
 }
-// A logit over the temperature, from its sum. The factors other than the
-// temperature's are exact.
+// A logit from its sum. The factors are powers of two.
 template <int DT>
-__device__ __forceinline__ float logit_of(float sum, float undo_h, float undo_w, float inv_temp) {
-  return DT == kF32 ? sum * undo_h * undo_w * inv_temp : sum * inv_temp;
+__device__ __forceinline__ float logit_of(float sum, const Head* head) {
+  return DT == kF32 ? sum * undo_h<DT>(head) * undo_w<DT>(head) : sum;
+}
+// What a logit's sum is multiplied by to be an exponent of two. (Where the scales
+// of both operands go out of fp32's range together, so do the logits: all zero.)
+template <int DT>
+__device__ __forceinline__ float exponent_factor(const Head* head, float inv_temp) {
+  const float f = inv_temp * kLog2e;
+  return DT == kF32 ? ldexpf(f, -scale_exponent(head->top_h) - scale_exponent(head->top_w)) : f;
 }
 
 // ---- The product ----------------------------------------------------------
@@ -843,7 +860,7 @@ __device__ __forceinline__ void Gather<DT>::wave(int64_t id) const {
   if (mine && q / 4 == lane / 16) {
     const float sum = q % 4 == 0 ? acc[0] : q % 4 == 1 ? acc[1] : q % 4 == 2 ? acc[2] : acc[3];
     const Head* head = reinterpret_cast<const Head*>(c.ws + p.o_head);
-    const float z = logit_of<DT>(sum, undo_h<DT>(head), undo_w<DT>(head), 1.0f);
+    const float z = logit_of<DT>(sum, head);
     (c.k == 0 ? reinterpret_cast<float*>(c.ws + p.o_entry) : c.logit)[t * K + k] = z;
   }
 }
@@ -858,8 +875,9 @@ __global__ void __launch_bounds__(256) gather_kernel(Gather<DT> g) {
 // m0 + 16 i + lane / 16 * 4 + 0..3.
 
 // Forward: the tile's rows m are vocabulary, its columns n live rows. Each wave
-// leaves the largest logit, the sum of exponentials and the sum of logits of
-// its stretch of the vocabulary.
+// leaves, of its stretch of the vocabulary, a base near its largest logit (as an
+// exponent of two), the sum of the exponentials relative to it, and the sum of
+// the logits' sums.
 // Sixteen columns of 128 results, four 16-bit values in a register pair (`part`,
 // one for each square), become rows of 256 bytes through 4 KB of LDS that are the
 // wave's own once the stages are done with: then a store has 16 bytes a lane and four whole rows, in place of 8 bytes
@@ -902,18 +920,15 @@ struct StatEpi {
     const int lane = threadIdx.x % 64;
     const int m_hi = vocab - m_base;
     if (m0 >= round_up_int(m_hi, (int)kStatRows) || n0 >= n_ext) return;
-    const float uh = undo_h<DT>(head), uw = undo_w<DT>(head);
+    const float f = exponent_factor<DT>(head, inv_temp);
     const bool edge = m0 + (int)kStatRows > m_hi;  // some of it is beyond the vocabulary
-    // The sums of exponentials are this kernel's second cost after the products (an
-    // exponential takes four times an addition), so what only some tiles need is
-    // kept out of the others' way.
+    // These exponentials are the kernel's second cost after the products: a maximum,
+    // one fused multiply-add, the power of two (four times an addition's time) and
+    // the sum are 26 cycles a logit, 3 us a tile that takes 16 for 768 inner steps.
+    // What only some tiles need is kept out of the others' way.
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
       float top = -INFINITY, total = 0.0f, plain = 0.0f;
-#pragma unroll
-      for (int i = 0; i < MI; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) acc[i][j][r] = logit_of<DT>(acc[i][j][r], uh, uw, inv_temp);
       if (sum != nullptr) {
 #pragma unroll
         for (int i = 0; i < MI; ++i)
@@ -935,11 +950,12 @@ struct StatEpi {
       }
       top = fmaxf(top, __shfl_xor(top, 16));
       top = fmaxf(top, __shfl_xor(top, 32));
-      const float from = top == -INFINITY ? 0.0f : top;  // -inf - -inf would be NaN
+      const float base = top == -INFINITY ? 0.0f : sixteenths(top * f);
 #pragma unroll
       for (int i = 0; i < MI; ++i)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) total += exp_f(acc[i][j][r] - from);
+        for (int r = 0; r < 4; ++r)
+          total += __builtin_amdgcn_exp2f(fmaf(acc[i][j][r], f, -base));
       total += __shfl_xor(total, 16);
       total += __shfl_xor(total, 32);
       const int n = n0 + j * 16 + lane % 16;
@@ -949,7 +965,7 @@ struct StatEpi {
         plain += __shfl_xor(plain, 32);
         if (lane < 16 && n < n_ext) sum[at] = plain;
       }
-      if (lane < 16 && n < n_ext) stat[at] = make_float2(top, total);
+      if (lane < 16 && n < n_ext) stat[at] = make_float2(base, total);
     }
   }
 };
@@ -974,7 +990,7 @@ struct GradEpi {
                                        lds_char* turn) {
     constexpr int kPlanes = DT == kF32 ? kParts : 1;
     const int lane = threadIdx.x % 64;
-    const float uh = undo_h<DT>(head), uw = undo_w<DT>(head);
+    const float f = exponent_factor<DT>(head, inv_temp);
     const bool edge = m0 + MI * 16 > m_ext || n0 + NJ * 16 > n_ext;
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
@@ -985,8 +1001,7 @@ struct GradEpi {
       for (int i = 0; i < MI; ++i)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          acc[i][j][r] =
-              rp.a * exp_f(logit_of<DT>(acc[i][j][r], uh, uw, inv_temp) - rp.lse);
+          acc[i][j][r] = rp.a2 * __builtin_amdgcn_exp2f(fmaf(acc[i][j][r], f, -rp.base));
       if (shift) {
 #pragma unroll
         for (int i = 0; i < MI; ++i) acc[i][j] -= rp.c;
@@ -996,7 +1011,7 @@ struct GradEpi {
         for (int i = 0; i < MI; ++i)
 #pragma unroll
           for (int r = 0; r < 4; ++r)
-            if (at == i * 16 + r) acc[i][j][r] -= rp.hit;
+            acc[i][j][r] -= at == i * 16 + r ? rp.hit : 0.0f;
       }
       if (edge) {
 #pragma unroll
@@ -1163,15 +1178,20 @@ __global__ void __launch_bounds__(256) loss_kernel(Call c) {
       for (int k = tid; k < K; k += 256) c.logit[t * K + k] = 0.0f;
     return;
   }
-  // largest logit m and sum s of exp(z - m) over the vocabulary
+  // base and sum s of 2^(z f - base) over the vocabulary, f = log2(e) / temperature
   const float2* stat = reinterpret_cast<const float2*>(c.ws + p.o_stat) + at * p.stat_cols;
   const int cols = (int)((p.vocab + kStatRows - 1) / kStatRows);
+  const Head* head = reinterpret_cast<const Head*>(c.ws + p.o_head);
   float m = -INFINITY;
-  for (int i = tid; i < cols; i += 256) m = fmaxf(m, stat[i].x);
+  for (int i = tid; i < cols; i += 256)
+    if (stat[i].y > 0.0f) m = fmaxf(m, stat[i].x);
   m = block_max<4>(m, red);
-  const float from = m == -INFINITY ? 0.0f : m;
+  if (m == -INFINITY) m = 0.0f;
   float s = 0.0f, plain = 0.0f;
-  for (int i = tid; i < cols; i += 256) s += stat[i].y * exp_f(stat[i].x - from);
+  for (int i = tid; i < cols; i += 256) {
+    const float2 q = stat[i];
+    s += q.y == 0.0f ? 0.0f : q.y * __builtin_amdgcn_exp2f(q.x - m);
+  }
   s = block_sum<4>(s, red);
   if (c.smoothing != 0.0f) {
     const float* sum = reinterpret_cast<const float*>(c.ws + p.o_sum) + at * p.stat_cols;
@@ -1179,20 +1199,27 @@ __global__ void __launch_bounds__(256) loss_kernel(Call c) {
     plain = block_sum<4>(plain, red);
   }
   const float* zs = (c.k == 0 ? reinterpret_cast<const float*>(c.ws + p.o_entry) : c.logit) + t * K;
-  const float logs = logf(s), lse = m + logs;
+  const float inv_temp = 1.0f / c.temperature, f = inv_temp * kLog2e;
+  const float log2s = log2f(s), lse = (float)(((double)m + log2s) * 0.6931471805599453);
+  // base - z f in one rounding: added to log2 s it is the loss in powers of two, and
+  // exact where the target is the largest logit, since the sum has the same term.
+  // (fp32's factor f of the sums is this one times a power of two.)
+  const auto behind = [m, f](float z) { return fmaf(-z, f, m); };
   if (c.k == 0) {
     if (tid == 0) {
       const float zy = zs[0];
-      // (m - zy) + log s: exact where the target is the largest logit
-      float loss = (m - zy) + logs;
-      if (c.smoothing != 0.0f) loss += c.smoothing * (zy - plain / (float)p.vocab);
+      float loss = (behind(zy) + log2s) * kLn2;
+      if (c.smoothing != 0.0f) {
+        const bool f32 = p.dtype == kF32;
+        plain = f32 ? logit_of<kF32>(plain, head) : plain;
+        loss += c.smoothing * (zy - plain / (float)p.vocab);
+      }
       if (c.z_loss != 0.0f) loss += c.z_loss * lse * lse;
       c.loss[t] = loss;
       c.lse[t] = lse;
     }
     return;
   }
-  const float inv_temp = 1.0f / c.temperature;
   float top = -INFINITY;
   for (int k = tid; k < K; k += 256) {
     const int64_t i = load_index(c.target, t * c.index_stride + k, c.index64);
@@ -1211,11 +1238,11 @@ __global__ void __launch_bounds__(256) loss_kernel(Call c) {
   for (int k = tid; k < K; k += 256) {
     const float lp = ls[k] - top - log_total;
     const float pk = exp_f(ls[k] - top) / total;
-    if (ls[k] != -INFINITY) kl += pk * (lp + (m - zs[k] * inv_temp));
+    if (ls[k] != -INFINITY) kl += pk * (lp + behind(zs[k]) * kLn2);
   }
   kl = block_sum<4>(kl, red);
   if (tid == 0) {
-    c.loss[t] = c.temperature * c.temperature * (kl + logs);
+    c.loss[t] = c.temperature * c.temperature * (kl + log2s * kLn2);
     c.lse[t] = lse;
   }
 }
