@@ -353,3 +353,22 @@ def test_gradients_land_in_a_worker_buffer_and_step():
     mean = zo.averaged_grad()[body.weight.numel():].view(301, 64).double()
     assert float((mean - total / 2).abs().max()) <= 2.0 ** -22 * float(total.abs().max())
     assert not torch.equal(before, head.detach())
+
+
+@pytest.mark.parametrize("precision", ["fp32", "bf16", "fp16"])
+def test_example_learns(precision):
+    """The example's both losses fall by more than half: gradients of the wrong sign,
+    scale or row would not do that."""
+    import os
+    import sys
+    say(f"[case] example {precision}")
+    at = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples")
+    sys.path.insert(0, at)
+    try:
+        import train_lm_head
+    finally:
+        sys.path.remove(at)
+    first, last = train_lm_head.train(steps=120, precision=precision, vocab=211)
+    say("  ", first, last)
+    for name in first:
+        assert math.isfinite(last[name]) and last[name] < first[name] / 2, (first, last)
