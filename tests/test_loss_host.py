@@ -213,3 +213,40 @@ def test_reference_distill_is_torchs():
     assert torch.allclose(r[0], loss.detach(), rtol=1e-12, atol=1e-12)
     assert torch.allclose(r[2], h.grad, rtol=1e-11, atol=1e-13)
     assert torch.allclose(r[3], w.grad, rtol=1e-11, atol=1e-13)
+
+
+def test_host_layer_under_sanitizers(tmp_path):
+    """zero_loss_abi.cpp with stub launchers over random shapes
+    (tests/sanitize/loss_driver.cpp), with AddressSanitizer and
+    UndefinedBehaviorSanitizer."""
+    import os
+    from test_sanitizers import ROOT, _build_and_run
+    csrc = os.path.join(ROOT, "zero_sharded_optimizer_amd", "csrc")
+    out = _build_and_run(tmp_path, "loss_driver",
+                         [os.path.join(ROOT, "tests", "sanitize", "loss_driver.cpp"),
+                          os.path.join(csrc, "zero_loss_abi.cpp"),
+                          os.path.join(csrc, "zero_abi.cpp")],
+                         includes=[os.path.join(ROOT, "include"), csrc])
+    assert "0 failures" in out
+
+
+def test_header_is_plain_c(tmp_path):
+    import os
+    import shutil
+    import subprocess
+    from test_sanitizers import ROOT
+    if shutil.which("gcc") is None:
+        pytest.skip("no gcc")
+    src = tmp_path / "h.c"
+    src.write_text('#include "zero_loss.h"\nint main(void) { return sizeof(zero_head) != 64 || '
+                   'sizeof(zero_xent_params) != 40 || sizeof(zero_distill_params) != 56 || '
+                   'sizeof(zero_head_grads) != 48; }\n')
+    exe = str(tmp_path / "h")
+    r = subprocess.run(["gcc", "-std=c99", "-pedantic", "-Wall", "-Werror",
+                        f"-I{os.path.join(ROOT, 'include')}", str(src), "-o", exe],
+                       capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    assert subprocess.run([exe]).returncode == 0
+    for c_type, size in ((_abi.zero_head, 64), (_abi.zero_xent_params, 40),
+                         (_abi.zero_distill_params, 56), (_abi.zero_head_grads, 48)):
+        assert C.sizeof(c_type) == size

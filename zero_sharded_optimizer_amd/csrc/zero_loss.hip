@@ -867,7 +867,10 @@ __device__ __forceinline__ void Gather<DT>::wave(int64_t id) const {
 
 template <int DT>
 __global__ void __launch_bounds__(256) gather_kernel(Gather<DT> g) {
-  g.wave((int64_t)blockIdx.x * 4 + threadIdx.x / 64);
+  const int64_t waves = g.waves();
+  for (int64_t id = (int64_t)blockIdx.x * 4 + threadIdx.x / 64; id < waves;
+       id += (int64_t)gridDim.x * 4)
+    g.wave(id);
 }
 
 // ---- What happens to a tile -------------------------------------------------
@@ -1447,7 +1450,8 @@ void loss_type(const Call& c, hipStream_t st) {
     // beside the tiles (8 to 13 us less). More would take the tiles' room in LDS.
     if (p.tokens <= kFewTokens) g.beside = (int)(blocks + 7) / 8 * 8;
     product<DT, false, false>(g, epi, st);
-    if (p.tokens > kFewTokens) gather_kernel<DT><<<(unsigned)blocks, 256, 0, st>>>(gather);
+    if (p.tokens > kFewTokens)
+      gather_kernel<DT><<<(unsigned)(blocks < (1 << 20) ? blocks : 1 << 20), 256, 0, st>>>(gather);
   }
   loss_kernel<<<(unsigned)p.tokens, 256, 0, st>>>(c);
 }

@@ -88,6 +88,7 @@ zero_status check_head(const zero_head* h) {
 int64_t choose_piece(const zloss::Plan& p, int64_t whole) {
   constexpr int64_t kPieceBytes = INT64_C(256) << 20;
   int64_t most = std::min<int64_t>(whole, INT64_C(1) << 21);
+  most = std::min(most, (INT64_C(1) << 38) / p.rows);
   if (p.grad) most = std::min(most, kPieceBytes / (p.rows * 2 * p.planes));
   if (p.pack_w) most = std::min(most, kPieceBytes / (p.dimp * 2 * p.planes));
   most = std::max<int64_t>(most / zloss::kVocPad * zloss::kVocPad, std::min<int64_t>(whole, 2048));
@@ -125,7 +126,9 @@ zloss::Plan make_plan(const zero_head& h, bool grad) {
   p.pack_w = p.planes > 1 || p.dimp != h.dim || h.weight_stride % 8 != 0 ||
              h.weight_stride > (INT64_C(1) << 22) || !aligned(h.weight, 16);
   const int64_t whole = round_up(h.vocab, zloss::kVocPad);
-  p.piece = whole;  // the loss of unpacked weights stores nothing of a piece
+  // The loss of unpacked weights stores nothing of a piece; but one launch has at
+  // most 2^22 tiles (2^31 work-items, of the 2^32 that it could describe).
+  p.piece = std::min(whole, (INT64_C(1) << 38) / p.rows / zloss::kVocPad * zloss::kVocPad);
   if (grad || p.pack_w) p.piece = choose_piece(p, whole);
   p.stat_cols = whole / zloss::kStatRows;
   // dhidden's sum over the vocabulary may be cut into slabs, as long as they are
