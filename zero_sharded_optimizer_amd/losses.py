@@ -38,7 +38,7 @@ import ctypes as C
 from dataclasses import dataclass
 
 from . import _abi
-from . import _raise, _same_device, _stream_handle
+from . import _raise, _stream_handle
 
 __all__ = ["Saved", "linear_xent", "linear_xent_grad", "linear_distill", "linear_distill_grad",
            "loss_workspace_bytes"]
@@ -46,6 +46,14 @@ __all__ = ["Saved", "linear_xent", "linear_xent_grad", "linear_distill", "linear
 _DTYPES = {"torch.float32": _abi.ZERO_LOSS_F32, "torch.bfloat16": _abi.ZERO_LOSS_BF16,
            "torch.float16": _abi.ZERO_LOSS_F16}
 _INDEX = {"torch.int32": _abi.ZERO_INDEX_I32, "torch.int64": _abi.ZERO_INDEX_I64}
+_codes = {}  # the same by torch.dtype, filled as types are met: their names take long to form
+
+
+def _code(dtype, table):
+    at = (dtype, table is _INDEX)
+    if at not in _codes:
+        _codes[at] = table.get(str(dtype))
+    return _codes[at]
 
 
 @dataclass
@@ -82,20 +90,21 @@ def _row_stride(x):
 def _head(hidden, weight):
     _matrix(hidden, "hidden")
     _matrix(weight, "weight", hidden.dtype)
-    if str(hidden.dtype) not in _DTYPES:
+    if _code(hidden.dtype, _DTYPES) is None:
         raise ValueError(f"hidden: dtype {hidden.dtype}, expected bfloat16, float16 or float32")
     if hidden.shape[1] != weight.shape[1]:
         raise ValueError(f"hidden has {hidden.shape[1]} columns, weight {weight.shape[1]}")
     return _abi.zero_head(tokens=hidden.shape[0], vocab=weight.shape[0], dim=hidden.shape[1],
                           hidden=hidden.data_ptr() or None, hidden_stride=_row_stride(hidden),
                           weight=weight.data_ptr() or None, weight_stride=_row_stride(weight),
-                          dtype=_DTYPES[str(hidden.dtype)], reserved=0)
+                          dtype=_code(hidden.dtype, _DTYPES), reserved=0)
 
 
 def _index_dtype(x, what):
-    if str(x.dtype) not in _INDEX:
+    code = _code(x.dtype, _INDEX)
+    if code is None:
         raise ValueError(f"{what}: dtype {x.dtype}, expected int32 or int64")
-    return _INDEX[str(x.dtype)]
+    return code
 
 
 def _xent_params(hidden, target, ignore_index, label_smoothing, z_loss):
@@ -119,13 +128,13 @@ def _distill_params(hidden, index, logit, temperature):
     _matrix(logit, "logit", shape=index.shape)
     if index.shape[0] != hidden.shape[0]:
         raise ValueError(f"index has {index.shape[0]} rows, hidden {hidden.shape[0]}")
-    if str(logit.dtype) not in _DTYPES:
+    if _code(logit.dtype, _DTYPES) is None:
         raise ValueError(f"logit: dtype {logit.dtype}, expected bfloat16, float16 or float32")
     return _abi.zero_distill_params(index=index.data_ptr() or None, logit=logit.data_ptr() or None,
                                     index_stride=_row_stride(index),
                                     logit_stride=_row_stride(logit), k=index.shape[1],
                                     index_dtype=_index_dtype(index, "index"),
-                                    logit_dtype=_DTYPES[str(logit.dtype)], reserved=0,
+                                    logit_dtype=_code(logit.dtype, _DTYPES), reserved=0,
                                     temperature=float(temperature))
 
 
@@ -142,16 +151,40 @@ def loss_workspace_bytes(hidden, weight, want_grad: bool) -> int:
     return _workspace_bytes(_head(hidden, weight), want_grad)
 
 
+def _one_device(stream, *xs):
+    """All tensors of a call (None left out) and a torch stream are on one GPU."""
+    dev = xs[0].device
+    for x in xs:
+        if x is not None and x.device != dev:
+            raise ValueError(f"all tensors of one call must be on one device, got {dev} and "
+                             f"{x.device}")
+    at = getattr(stream, "device", dev)
+    if at != dev:
+        raise ValueError(f"stream is on {at}, the tensors on {dev}")
+
+
+class _NoContext:
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return False
+
+
+_NO_CONTEXT = _NoContext()
+
+
 def _on_stream(stream, hidden):
-    """A context in which torch allocates for `stream`: memory given back after
-    the call is then reused in that stream's order."""
-    import contextlib
+    """A context on hidden's device in which torch allocates for `stream`: memory
+    given back after the call is then reused in that stream's order."""
     import torch
     if stream is None:
-        return contextlib.nullcontext()
+        if torch.cuda.current_device() == hidden.device.index:
+            return _NO_CONTEXT
+        return torch.cuda.device(hidden.device)
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=hidden.device)
-    return torch.cuda.stream(stream)
+    return torch.cuda.stream(stream)  # also makes its device the current one
 
 
 def _workspace(head, want_grad, workspace, like):
@@ -171,9 +204,9 @@ def linear_xent(hidden, weight, target, ignore_index: int = -100, label_smoothin
     import torch
     head = _head(hidden, weight)
     params = _xent_params(hidden, target, ignore_index, label_smoothing, z_loss)
-    _same_device(stream, hidden, weight, target, workspace)
+    _one_device(stream, hidden, weight, target, workspace)
     lib = _abi.load()
-    with torch.cuda.device(hidden.device), _on_stream(stream, hidden):
+    with _on_stream(stream, hidden):
         loss = torch.empty(hidden.shape[0], dtype=torch.float32, device=hidden.device)
         lse = torch.empty_like(loss)
         ws, nbytes = _workspace(head, False, workspace, hidden)
@@ -192,9 +225,9 @@ def linear_distill(hidden, weight, index, logit, temperature: float = 1.0, works
     import torch
     head = _head(hidden, weight)
     params = _distill_params(hidden, index, logit, temperature)
-    _same_device(stream, hidden, weight, index, logit, workspace)
+    _one_device(stream, hidden, weight, index, logit, workspace)
     lib = _abi.load()
-    with torch.cuda.device(hidden.device), _on_stream(stream, hidden):
+    with _on_stream(stream, hidden):
         loss = torch.empty(hidden.shape[0], dtype=torch.float32, device=hidden.device)
         lse = torch.empty_like(loss)
         kept = torch.empty(index.shape, dtype=torch.float32, device=hidden.device)
@@ -242,8 +275,9 @@ def _grad(entry, hidden, weight, head, params, saved, extra, upstream, dhidden, 
     if dweight is not None:
         _matrix(dweight, "dweight", weight.dtype, weight.shape)
     _check_saved(saved.lse, "saved.lse", (hidden.shape[0],))
-    _same_device(stream, hidden, weight, tensors, saved.lse, upstream, dhidden, dweight, workspace)
-    with torch.cuda.device(hidden.device), _on_stream(stream, hidden):
+    _one_device(stream, hidden, weight, *tensors, saved.lse, dhidden, dweight, workspace,
+                upstream if isinstance(upstream, torch.Tensor) else None)
+    with _on_stream(stream, hidden):
         up, up_stride = _upstream(upstream, hidden)
         if need_dhidden and dhidden is None:
             dhidden = torch.empty(hidden.shape, dtype=hidden.dtype, device=hidden.device)
