@@ -537,7 +537,7 @@ struct Product {
   const Head* head;
 };
 
-// 256 x BN tiles, inner steps of 64, two LDS stages that global memory is copied
+// BM x BN tiles, inner steps of 64, two LDS stages that global memory is copied
 // into directly while the other is multiplied. Waves hold 128 x (BN / 4 or 32)
 // of the tile in matrix instructions 16x16x32.
 //
@@ -550,16 +550,27 @@ struct Product {
 typedef __attribute__((address_space(3))) char lds_char;
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
-template <int BN>
+template <int BM, int BN>
 struct Shape {
   static constexpr int kWaveN = BN == 256 ? 64 : 32;
-  static constexpr int kWaves = 2 * (BN / kWaveN);
+  static constexpr int kWavesM = BM / 128;
+  static constexpr int kWaves = kWavesM * (BN / kWaveN);
   static constexpr int kThreads = 64 * kWaves;
-  static constexpr int kStage = (256 + BN) * 128;  // bytes
+  static constexpr int kStageB = BM * 128;         // bytes before a stage's right operand
+  static constexpr int kStage = (BM + BN) * 128;
 };
 
-// The inner step that the logits' narrow tiles of vocabulary row m start at.
-__device__ __forceinline__ int first_step(int m, int steps) { return m / 256 * 5 % steps; }
+// Few tokens: the weight's way from memory is all that counts. A vocabulary whose
+// tiles of 256 rows would leave half of the chip's compute units without one is cut
+// into tiles of 128: 32000 x 4096 takes 58 us in place of 67, while 50257 x 4096 and
+// more are faster in 256 (89 in place of 98).
+__host__ __device__ __forceinline__ int few_tile_rows(int vocab_rows) {
+  return (vocab_rows + 255) / 256 <= 128 ? 128 : 256;
+}
+// The inner step that such a tile, from vocabulary row m on, starts at.
+__device__ __forceinline__ int first_step(int m, int tile_rows, int steps) {
+  return m / tile_rows * 5 % steps;
+}
 
 // Byte offsets, from the tile's corner (r0 < o.rows: a tile starts on a real row), that lane `l` of wave `w` copies from
 // with its i-th instruction of 64 groups.
@@ -613,11 +624,11 @@ __device__ __forceinline__ u32x4 fragment(lds_char* tile, int at, int ks, int la
   }
 }
 
-template <int DT, bool TA, bool TB, int BN, class Epi>
-__global__ void __launch_bounds__(Shape<BN>::kThreads, 2) product_kernel(Product g, Epi epi) {
-  using S = Shape<BN>;
+template <int DT, bool TA, bool TB, int BM, int BN, class Epi>
+__global__ void __launch_bounds__((Shape<BM, BN>::kThreads), 2) product_kernel(Product g, Epi epi) {
+  using S = Shape<BM, BN>;
   constexpr int MI = 8, NJ = S::kWaveN / 16;
-  constexpr int kCopyA = 32 / S::kWaves, kCopyB = BN / 8 / S::kWaves;
+  constexpr int kCopyA = BM / 8 / S::kWaves, kCopyB = BN / 8 / S::kWaves;
   __shared__ __attribute__((aligned(1024))) char smem[2 * S::kStage];
   lds_char* lds = (lds_char*)smem;
   const uint32_t lds_at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds);
@@ -630,7 +641,7 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, 2) product_kernel(Product
   // Tiles are numbered in strips four columns wide, and each of the chip's eight
   // dies (blocks go to them in turn) gets a run of them, so that the tiles in
   // flight on a die share rows and columns in its cache.
-  const int mt = (g.m + 255) / 256, nt = (n_ext + BN - 1) / BN;
+  const int mt = (g.m + BM - 1) / BM, nt = (n_ext + BN - 1) / BN;
   const int splits = g.split ? g.head->splits : 1;
   const int total = mt * nt * splits, run = (total + 7) / 8;
   int id = (int)blockIdx.x - g.beside;
@@ -642,17 +653,17 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, 2) product_kernel(Product
   id -= split * mt * nt;
   const int strip = id / (4 * mt), wide = min(4, nt - strip * 4);
   id -= strip * 4 * mt;
-  const int m0 = id / wide * 256, n0 = (strip * 4 + id % wide) * BN;
+  const int m0 = id / wide * BM, n0 = (strip * 4 + id % wide) * BN;
 
   const int chunk = round_up_int((inner + splits - 1) / splits, 64);
   const int k_lo = min(inner, split * chunk), k_hi = min(inner, k_lo + chunk);
   const int steps = (k_hi - k_lo) / 64, all = steps * g.segs;
-  const int wm = (wave & 1) * 128, wn = (wave >> 1) * S::kWaveN;
+  const int wm = wave % S::kWavesM * 128, wn = wave / S::kWavesM * S::kWaveN;
 
   uint32_t oa[kCopyA], ob[kCopyB];
 #pragma unroll
   for (int i = 0; i < kCopyA; ++i)
-    oa[i] = copy_offset<TA, 256>(g.a, m0, wave * kCopyA + i, lane);
+    oa[i] = copy_offset<TA, BM>(g.a, m0, wave * kCopyA + i, lane);
 #pragma unroll
   for (int i = 0; i < kCopyB; ++i)
     ob[i] = copy_offset<TB, BN>(g.b, n0, wave * kCopyB + i, lane);
@@ -667,7 +678,7 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, 2) product_kernel(Product
   // two apart more often than not, and blocks that all read the same columns would
   // ask the same channels: each row of tiles starts at another step and comes round.
   constexpr bool kTurned = BN == 64 && !TA && !TB;
-  const int turn = kTurned && steps > 0 ? first_step(m0, steps) : 0;
+  const int turn = kTurned && steps > 0 ? first_step(m0, BM, steps) : 0;
   int seg = 0, at = turn;  // the next step to copy
   pa += turn * step_a;
   pb += turn * step_b;
@@ -675,7 +686,7 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, 2) product_kernel(Product
   const auto copy_part = [&](int stage, int i) INLINE {
     const uint32_t to = lds_at + stage * S::kStage;
     if (i < kCopyA) copy_to_lds(pa, oa[i], to + (wave * kCopyA + i) * 1024);
-    else copy_to_lds(pb, ob[i - kCopyA], to + 32768 + (wave * kCopyB + i - kCopyA) * 1024);
+    else copy_to_lds(pb, ob[i - kCopyA], to + S::kStageB + (wave * kCopyB + i - kCopyA) * 1024);
   };
   const auto before_copy = [&]() INLINE {
     if (TA && k_lo + at * 64 + 64 > g.a.steps) {
@@ -684,7 +695,7 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, 2) product_kernel(Product
       for (int i = 0; i < kCopyA; ++i) {
         const int k = (wave * kCopyA + i) * 2 + lane / 32;
         const int over = max(0, k_lo + at * 64 + k - (g.a.steps - 1));
-        oa[i] = copy_offset<TA, 256>(g.a, m0, wave * kCopyA + i, lane) -
+        oa[i] = copy_offset<TA, BM>(g.a, m0, wave * kCopyA + i, lane) -
                 (uint32_t)over * (uint32_t)(g.a.ld * 2);
       }
     }
@@ -705,7 +716,7 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, 2) product_kernel(Product
         if constexpr (TA) {
 #pragma unroll
           for (int i = 0; i < kCopyA; ++i)
-            oa[i] = copy_offset<TA, 256>(g.a, m0, wave * kCopyA + i, lane);
+            oa[i] = copy_offset<TA, BM>(g.a, m0, wave * kCopyA + i, lane);
         }
       }
     }
@@ -723,7 +734,7 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads, 2) product_kernel(Product
   const auto read_part = [&](int stage, int ks, int q, u32x4 (&fa)[MI], u32x4 (&fb)[NJ]) INLINE {
     lds_char* ta = lds + stage * S::kStage;
     if (q == 1) fa[0] = fragment<TA>(ta, wm, ks, lane);
-    else if (q <= NJ) fb[q == 0 ? 0 : q - 1] = fragment<TB>(ta + 32768, wn + (q == 0 ? 0 : q - 1) * 16, ks, lane);
+    else if (q <= NJ) fb[q == 0 ? 0 : q - 1] = fragment<TB>(ta + S::kStageB, wn + (q == 0 ? 0 : q - 1) * 16, ks, lane);
     else fa[q - NJ] = fragment<TA>(ta, wm + (q - NJ) * 16, ks, lane);
   };
   // Multiplies one half step, row by row of the wave's tile, and between the rows
@@ -837,7 +848,7 @@ __device__ __forceinline__ void Gather<DT>::wave(int64_t id) const {
                  (int64_t)min(row, live - 1) * p.dimp + lane / 16 * 8;
   const u16* a = w + (mine ? m : 0) * ldw + lane / 16 * 8;
   // the narrow tiles' order of steps, each pair in that of its own weight row
-  const int turn = p.tokens <= kFewTokens && mine ? first_step((int)m, (int)p.dimp / 64) * 64 : 0;
+  const int turn = p.tokens <= kFewTokens && mine ? first_step((int)m, few_tile_rows(real), (int)p.dimp / 64) * 64 : 0;
   f32x4 acc = {};
   for (int seg = 0; seg < (DT == kF32 ? kSegs : 1); ++seg) {
     const u16* pa = a + (DT == kF32 ? seg_a(seg) * p.piece * p.dimp : 0);
@@ -1356,12 +1367,12 @@ bool rows_aligned(const void* p, int64_t stride, int dt, int n) {
   return aligned(p, (uintptr_t)(n * element(dt))) && stride % n == 0;
 }
 
-template <int DT, bool TA, bool TB, int BN, class Epi>
+template <int DT, bool TA, bool TB, int BM, int BN, class Epi>
 void product_tiles(const Product& g, const Epi& epi, int64_t most_split, hipStream_t st) {
-  int64_t total = (int64_t)((g.m + 255) / 256) * ((g.n + BN - 1) / BN);
+  int64_t total = (int64_t)((g.m + BM - 1) / BM) * ((g.n + BN - 1) / BN);
   if (g.split && total < most_split) total = most_split;
-  product_kernel<DT, TA, TB, BN, Epi>
-      <<<(unsigned)((total + 7) / 8 * 8 + g.beside), Shape<BN>::kThreads, 0, st>>>(g, epi);
+  product_kernel<DT, TA, TB, BM, BN, Epi>
+      <<<(unsigned)((total + 7) / 8 * 8 + g.beside), Shape<BM, BN>::kThreads, 0, st>>>(g, epi);
 }
 
 // Columns are tokens (few of them take narrower tiles) or, where the right
@@ -1369,9 +1380,15 @@ void product_tiles(const Product& g, const Epi& epi, int64_t most_split, hipStre
 template <int DT, bool TA, bool TB, class Epi>
 void product(const Product& g, const Epi& epi, hipStream_t st, int64_t most_split = 0) {
   if constexpr (!TB) {
-    if (g.n_real <= kFewTokens) return product_tiles<DT, TA, TB, 64, Epi>(g, epi, most_split, st);
+    if (g.n_real <= kFewTokens) {
+      if constexpr (!TA) {
+        if (few_tile_rows(g.m) == 128)
+          return product_tiles<DT, TA, TB, 128, 64, Epi>(g, epi, most_split, st);
+      }
+      return product_tiles<DT, TA, TB, 256, 64, Epi>(g, epi, most_split, st);
+    }
   }
-  product_tiles<DT, TA, TB, 256, Epi>(g, epi, most_split, st);
+  product_tiles<DT, TA, TB, 256, 256, Epi>(g, epi, most_split, st);
 }
 
 template <int DT>
@@ -1445,10 +1462,10 @@ void loss_type(const Call& c, hipStream_t st) {
                     c.smoothing != 0.0f ? reinterpret_cast<float*>(c.ws + p.o_sum) : nullptr,
                     p.stat_cols, 1.0f / c.temperature, (int)v0, (int)p.vocab};
     Product g = logits_product<DT>(c, w, ldw, real);
-    const int64_t blocks = (gather.waves() + 3) / 4;
+    const int64_t blocks = (gather.waves() + 3) / 4, pairs = (gather.waves() + 1) / 2;
     // Few tokens: the gather's few waves, which wait for memory ten times over, go
     // beside the tiles (8 to 13 us less). More would take the tiles' room in LDS.
-    if (p.tokens <= kFewTokens) g.beside = (int)(blocks + 7) / 8 * 8;
+    if (p.tokens <= kFewTokens) g.beside = (int)(pairs + 7) / 8 * 8;
     product<DT, false, false>(g, epi, st);
     if (p.tokens > kFewTokens)
       gather_kernel<DT><<<(unsigned)(blocks < (1 << 20) ? blocks : 1 << 20), 256, 0, st>>>(gather);
