@@ -528,7 +528,7 @@ struct Operand {
 struct Product {
   Operand a, b;
   int m, n;        // extents (n: the most there can be, where live_n)
-  int n_real;      // columns that mean something
+  int n_real, inner_real;  // columns and inner steps that may mean something, at most
   int inner;       // inner extent, a multiple of 64 (the most there can be, where live_inner)
   bool live_n, live_inner;  // the extent is the live count, rounded up to 64 for the inner one
   bool split;      // the inner extent is cut into head->splits runs
@@ -537,12 +537,12 @@ struct Product {
   const Head* head;
 };
 
-// BM x BN tiles, inner steps of 64, two LDS stages that global memory is copied
+// BM x BN tiles, inner steps of 64, one or two LDS stages that global memory is copied
 // into directly while the other is multiplied. Waves hold 128 x (BN / 4 or 32)
 // of the tile in matrix instructions 16x16x32.
 //
 // LDS holds a tile as it lies in memory, rows of 128 bytes (inner index
-// contiguous) or 512 bytes (rows contiguous), in 16-byte groups whose place in
+// contiguous) or 2 BM, 2 BN bytes (rows contiguous), in 16-byte groups whose place in
 // their row is exchanged by a function of the row, so that the lanes of one read
 // fall on different banks. The copy writes lane after lane, so the exchange is
 // made in the addresses it reads from. A transposed tile is turned by the
@@ -550,7 +550,7 @@ struct Product {
 typedef __attribute__((address_space(3))) char lds_char;
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
-template <int BM, int BN>
+template <int BM, int BN, int STAGES>
 struct Shape {
   static constexpr int kWaveN = BN == 256 ? 64 : 32;
   static constexpr int kWavesM = BM / 128;
@@ -558,6 +558,7 @@ struct Shape {
   static constexpr int kThreads = 64 * kWaves;
   static constexpr int kStageB = BM * 128;         // bytes before a stage's right operand
   static constexpr int kStage = (BM + BN) * 128;
+  static constexpr int kLds = STAGES * kStage;
 };
 
 // Few tokens: the weight's way from memory is all that counts. A vocabulary whose
@@ -581,10 +582,10 @@ __device__ __forceinline__ uint32_t copy_offset(const Operand& o, int r0, int in
     const int group = (lane % 8) ^ (lane / 8);
     return (uint32_t)(min(r0 + r, o.rows - 1) - r0) * (uint32_t)(o.ld * 2) + group * 16;
   } else {
-    static_assert(R == 256, "two inner steps an instruction");
-    const int k = instr * 2 + lane / 32;
+    constexpr int kGroups = R / 8;  // in an inner step's row
+    const int k = instr * (64 / kGroups) + lane / kGroups;
     const int turn = (k & 3) | ((k >> 3) & 1) << 2;
-    const int group = (lane % 32) ^ (turn << 1);
+    const int group = (lane % kGroups) ^ (turn << 1);
     return (uint32_t)k * (uint32_t)(o.ld * 2) + (uint32_t)(min(r0 + group * 8, o.rows - 8) - r0) * 2;
   }
 }
@@ -605,7 +606,7 @@ __device__ __forceinline__ void copy_to_lds(const char* base, uint32_t offset, u
 
 // The operand registers of one matrix instruction: 16 rows from `at`, inner
 // steps 32 ks + lane / 16 * 8 + 0..7.
-template <bool T>
+template <bool T, int R>
 __device__ __forceinline__ u32x4 fragment(lds_char* tile, int at, int ks, int lane) {
   if constexpr (!T) {
     const int off = (at + lane % 16) * 128 + (((ks * 4 + lane / 16) ^ (lane & 7)) * 16);
@@ -613,23 +614,23 @@ __device__ __forceinline__ u32x4 fragment(lds_char* tile, int at, int ks, int la
   } else {
     const int i = lane % 16, g = lane / 16;
     const int turn = (i / 4) | (g & 1) << 2;
-    const int off = (ks * 32 + g * 8 + i / 4) * 512 + (((at / 16) ^ turn) * 32) + (i % 4) * 8;
+    const int off = (ks * 32 + g * 8 + i / 4) * (R * 2) + (((at / 16) ^ turn) * 32) + (i % 4) * 8;
     typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
     const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
         reinterpret_cast<lds_s16x4*>(tile + off));
     const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-        reinterpret_cast<lds_s16x4*>(tile + off + 4 * 512));
+        reinterpret_cast<lds_s16x4*>(tile + off + 4 * (R * 2)));
     const u32x2 a = __builtin_bit_cast(u32x2, lo), b = __builtin_bit_cast(u32x2, hi);
     return u32x4{a[0], a[1], b[0], b[1]};
   }
 }
 
-template <int DT, bool TA, bool TB, int BM, int BN, class Epi>
-__global__ void __launch_bounds__((Shape<BM, BN>::kThreads), 2) product_kernel(Product g, Epi epi) {
-  using S = Shape<BM, BN>;
+template <int DT, bool TA, bool TB, int BM, int BN, int STAGES, class Epi>
+__global__ void __launch_bounds__((Shape<BM, BN, STAGES>::kThreads), 2) product_kernel(Product g, Epi epi) {
+  using S = Shape<BM, BN, STAGES>;
   constexpr int MI = 8, NJ = S::kWaveN / 16;
   constexpr int kCopyA = BM / 8 / S::kWaves, kCopyB = BN / 8 / S::kWaves;
-  __shared__ __attribute__((aligned(1024))) char smem[2 * S::kStage];
+  __shared__ __attribute__((aligned(1024))) char smem[S::kLds];
   lds_char* lds = (lds_char*)smem;
   const uint32_t lds_at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds);
 
@@ -693,7 +694,7 @@ __global__ void __launch_bounds__((Shape<BM, BN>::kThreads), 2) product_kernel(P
       // the weight's last rows: there are no more, and the other operand holds zeros
 #pragma unroll
       for (int i = 0; i < kCopyA; ++i) {
-        const int k = (wave * kCopyA + i) * 2 + lane / 32;
+        const int k = (wave * kCopyA + i) * (512 / BM) + lane / (BM / 8);
         const int over = max(0, k_lo + at * 64 + k - (g.a.steps - 1));
         oa[i] = copy_offset<TA, BM>(g.a, m0, wave * kCopyA + i, lane) -
                 (uint32_t)over * (uint32_t)(g.a.ld * 2);
@@ -733,9 +734,9 @@ __global__ void __launch_bounds__((Shape<BM, BN>::kThreads), 2) product_kernel(P
   // Operand q of a half step, in the order the matrix instructions want them.
   const auto read_part = [&](int stage, int ks, int q, u32x4 (&fa)[MI], u32x4 (&fb)[NJ]) INLINE {
     lds_char* ta = lds + stage * S::kStage;
-    if (q == 1) fa[0] = fragment<TA>(ta, wm, ks, lane);
-    else if (q <= NJ) fb[q == 0 ? 0 : q - 1] = fragment<TB>(ta + S::kStageB, wn + (q == 0 ? 0 : q - 1) * 16, ks, lane);
-    else fa[q - NJ] = fragment<TA>(ta, wm + (q - NJ) * 16, ks, lane);
+    if (q == 1) fa[0] = fragment<TA, BM>(ta, wm, ks, lane);
+    else if (q <= NJ) fb[q == 0 ? 0 : q - 1] = fragment<TB, BN>(ta + S::kStageB, wn + (q == 0 ? 0 : q - 1) * 16, ks, lane);
+    else fa[q - NJ] = fragment<TA, BM>(ta, wm + (q - NJ) * 16, ks, lane);
   };
   // Multiplies one half step, row by row of the wave's tile, and between the rows
   // reads the next half's operands (read_stage >= 0) and copies the next free
@@ -1367,12 +1368,12 @@ bool rows_aligned(const void* p, int64_t stride, int dt, int n) {
   return aligned(p, (uintptr_t)(n * element(dt))) && stride % n == 0;
 }
 
-template <int DT, bool TA, bool TB, int BM, int BN, class Epi>
+template <int DT, bool TA, bool TB, int BM, int BN, int STAGES, class Epi>
 void product_tiles(const Product& g, const Epi& epi, int64_t most_split, hipStream_t st) {
   int64_t total = (int64_t)((g.m + BM - 1) / BM) * ((g.n + BN - 1) / BN);
   if (g.split && total < most_split) total = most_split;
-  product_kernel<DT, TA, TB, BM, BN, Epi>
-      <<<(unsigned)((total + 7) / 8 * 8 + g.beside), Shape<BM, BN>::kThreads, 0, st>>>(g, epi);
+  product_kernel<DT, TA, TB, BM, BN, STAGES, Epi>
+      <<<(unsigned)((total + 7) / 8 * 8 + g.beside), Shape<BM, BN, STAGES>::kThreads, 0, st>>>(g, epi);
 }
 
 // Columns are tokens (few of them take narrower tiles) or, where the right
@@ -1383,12 +1384,17 @@ void product(const Product& g, const Epi& epi, hipStream_t st, int64_t most_spli
     if (g.n_real <= kFewTokens) {
       if constexpr (!TA) {
         if (few_tile_rows(g.m) == 128)
-          return product_tiles<DT, TA, TB, 128, 64, Epi>(g, epi, most_split, st);
+          return product_tiles<DT, TA, TB, 128, 64, 2, Epi>(g, epi, most_split, st);
       }
-      return product_tiles<DT, TA, TB, 256, 64, Epi>(g, epi, most_split, st);
+      return product_tiles<DT, TA, TB, 256, 64, 2, Epi>(g, epi, most_split, st);
     }
   }
-  product_tiles<DT, TA, TB, 256, 256, Epi>(g, epi, most_split, st);
+  if constexpr (TB) {
+    // at most one inner step: what counts is the result's way to memory
+    if (g.inner_real <= 64 && g.segs == 1)
+      return product_tiles<DT, TA, TB, 128, 256, 1, Epi>(g, epi, most_split, st);
+  }
+  product_tiles<DT, TA, TB, 256, 256, 2, Epi>(g, epi, most_split, st);
 }
 
 template <int DT>
@@ -1515,6 +1521,7 @@ void grad_type(const Call& c, hipStream_t st) {
       d.m = (int)p.dimp;
       d.n = (int)real;
       d.inner = (int)p.rows;
+      d.inner_real = (int)p.tokens;
       d.live_inner = true;
       d.segs = g.segs;
       d.head = head;
