@@ -250,16 +250,36 @@ __device__ __forceinline__ RowParam row_param(const Call& c, int64_t t, float sc
   return rp;
 }
 
-// dhidden has few tiles, [live, dim], and a long sum, over the piece's vocabulary:
-// the sum is cut into as many runs as make the rounds of 256 tiles that the chip
-// holds at once end soonest, a round taking the run's steps and about four more.
-// Lane l of the wave looks at l + 1 runs.
-__device__ __forceinline__ int choose_splits(const Plan& p, int live) {
-  const int lane = threadIdx.x % 64, s = lane + 1;
-  const int bn = p.tokens <= kFewTokens ? 64 : 256, held = p.tokens <= kFewTokens ? 512 : 256;
-  const int tiles = (live + bn - 1) / bn * (int)((p.dimp + 255) / 256);
-  const int steps = ((int)(p.piece / 64) + s - 1) / s;
-  int cost = (tiles * s + held - 1) / held * (steps + 4);
+// dhidden has few tiles, [live, dim], and a long sum, over the piece's vocabulary,
+// which may be cut into runs. A tile takes its run's steps and about four more. Few
+// tokens: the number of runs with which the rounds of 512 tiles that the chip holds
+// at once end soonest. Else the tiles are started as dweight's of the same launch
+// end: `full` rounds of 256, and `rest` in one more; they are done at the first time
+// at which the units that were free from the start of that round, and those that
+// were from its end, have had time for them all. Lane l looks at l + 1 runs.
+__device__ __forceinline__ int choose_splits(const Call& c, int live) {
+  const Plan& p = c.plan;
+  const bool few = p.tokens <= kFewTokens;
+  const int lane = threadIdx.x % 64, s = lane + 1, bn = few ? 64 : 256;
+  const int across = (int)((p.dimp + 255) / 256);
+  const int tiles = (live + bn - 1) / bn * across;
+  const int steps = ((int)(p.piece / 64) + s - 1) / s, each = steps + 4;
+  int cost;
+  if (few) {
+    cost = (tiles * s + 511) / 512 * each;
+  } else {
+    const int w_tiles = c.dweight != nullptr ? (int)(p.piece / 256) * across : 0;
+    const int w_each = (live + 63) / 64 + 4;
+    const int full = w_tiles / 256, rest = w_tiles % 256;
+    // k tiles on each early unit, and what the late ones manage in that time
+    int k = max(1, tiles * s / 256);
+    const auto done = [&](int t) {
+      return (256 - rest) * (t / each) + rest * (max(0, t - w_each) / each);
+    };
+    int t = k * each;
+    while (done(t) < tiles * s) t += min(each, rest > 0 ? w_each : each);
+    cost = full * w_each + max(t, rest > 0 ? w_each : 0);
+  }
   if (s > 1 && (tiles * s > p.acc_tiles || steps < 4)) cost = 0x7fffffff;
   int best = cost;
 #pragma unroll
@@ -306,7 +326,7 @@ __global__ void __launch_bounds__(1024) scan_kernel(Call c) {
     }
     base += total;
   }
-  const int splits = c.plan.grad && wave == 0 ? choose_splits(c.plan, base) : 1;
+  const int splits = c.plan.grad && wave == 0 ? choose_splits(c, base) : 1;
   reach = {wave_max(reach.top), wave_max(reach.pull)};
   if (lane == 0) reaches[wave] = reach;
   __syncthreads();
@@ -446,7 +466,7 @@ __global__ void __launch_bounds__(256) few_rows_kernel(Call c, bool wide) {
       if (st == kLive) reinterpret_cast<int*>(c.ws + p.o_rowmap)[at] = lane;
       if (lane < tokens)
         reinterpret_cast<int*>(c.ws + p.o_pos)[lane] = st == kLive ? at : st == kEmpty ? -1 : -2;
-      const int splits = p.grad ? choose_splits(p, live) : 1;
+      const int splits = p.grad ? choose_splits(c, live) : 1;
       Reach r = {0.0f, 0.0f};
       if (p.grad && st == kLive) r = row_reach(c, lane);
       r = {wave_max(r.top), wave_max(r.pull)};
@@ -626,11 +646,11 @@ __device__ __forceinline__ u32x4 fragment(lds_char* tile, int at, int ks, int la
 }
 
 template <int DT, bool TA, bool TB, int BM, int BN, int STAGES, class Epi>
-__global__ void __launch_bounds__((Shape<BM, BN, STAGES>::kThreads), 2) product_kernel(Product g, Epi epi) {
+__device__ __forceinline__ void product_block(const Product& g, Epi epi, int block,
+                                              char* smem) {
   using S = Shape<BM, BN, STAGES>;
   constexpr int MI = 8, NJ = S::kWaveN / 16;
   constexpr int kCopyA = BM / 8 / S::kWaves, kCopyB = BN / 8 / S::kWaves;
-  __shared__ __attribute__((aligned(1024))) char smem[S::kLds];
   lds_char* lds = (lds_char*)smem;
   const uint32_t lds_at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds);
 
@@ -645,8 +665,8 @@ __global__ void __launch_bounds__((Shape<BM, BN, STAGES>::kThreads), 2) product_
   const int mt = (g.m + BM - 1) / BM, nt = (n_ext + BN - 1) / BN;
   const int splits = g.split ? g.head->splits : 1;
   const int total = mt * nt * splits, run = (total + 7) / 8;
-  int id = (int)blockIdx.x - g.beside;
-  if (id < 0) return epi.beside((int64_t)blockIdx.x * S::kWaves + wave);
+  int id = block - g.beside;
+  if (id < 0) return epi.beside((int64_t)block * S::kWaves + wave);
   if (id / 8 >= run) return;
   id = (id % 8) * run + id / 8;
   if (id >= total) return;
@@ -807,6 +827,13 @@ __global__ void __launch_bounds__((Shape<BM, BN, STAGES>::kThreads), 2) product_
   }
   epi.template tile<MI, NJ>(m0 + wm, n0 + wn, n_ext, split, acc,
                             lds + wave * 4096);
+}
+
+template <int DT, bool TA, bool TB, int BM, int BN, int STAGES, class Epi>
+__global__ void __launch_bounds__((Shape<BM, BN, STAGES>::kThreads), 2)
+    product_kernel(Product g, Epi epi) {
+  __shared__ __attribute__((aligned(1024))) char smem[Shape<BM, BN, STAGES>::kLds];
+  product_block<DT, TA, TB, BM, BN, STAGES, Epi>(g, epi, (int)blockIdx.x, smem);
 }
 
 // ---- The targets' logits ----------------------------------------------------
@@ -1154,6 +1181,19 @@ struct WeightEpi {
   }
 };
 
+// Both products over a piece's g in one launch, dweight's tiles first: its last round
+// of tiles seldom fills the chip, and dhidden's, whose size choose_splits() picks, go
+// beside it. (4095 x 50257 x 768: two launches took 690 us, this one 600.)
+template <int DT>
+__global__ void __launch_bounds__(512, 2)
+    gradients_kernel(Product w, WeightEpi<DT> we, int first, Product d, SumEpi de) {
+  __shared__ __attribute__((aligned(1024))) char smem[Shape<256, 256, 2>::kLds];
+  if ((int)blockIdx.x < first)
+    product_block<DT, true, true, 256, 256, 2, WeightEpi<DT>>(w, we, (int)blockIdx.x, smem);
+  else
+    product_block<DT, true, false, 256, 256, 2, SumEpi>(d, de, (int)blockIdx.x - first, smem);
+}
+
 // ---- Rows: the losses -------------------------------------------------------
 template <int N>
 __device__ __forceinline__ float block_max(float x, float* s) {
@@ -1377,24 +1417,23 @@ void product_tiles(const Product& g, const Epi& epi, int64_t most_split, hipStre
 }
 
 // Columns are tokens (few of them take narrower tiles) or, where the right
-// operand is transposed, vocabulary.
+// operand is transposed, vocabulary. (dhidden and dweight of more tokens share a
+// launch of their own.)
 template <int DT, bool TA, bool TB, class Epi>
 void product(const Product& g, const Epi& epi, hipStream_t st, int64_t most_split = 0) {
-  if constexpr (!TB) {
-    if (g.n_real <= kFewTokens) {
-      if constexpr (!TA) {
-        if (few_tile_rows(g.m) == 128)
-          return product_tiles<DT, TA, TB, 128, 64, 2, Epi>(g, epi, most_split, st);
-      }
-      return product_tiles<DT, TA, TB, 256, 64, 2, Epi>(g, epi, most_split, st);
-    }
-  }
   if constexpr (TB) {
-    // at most one inner step: what counts is the result's way to memory
-    if (g.inner_real <= 64 && g.segs == 1)
-      return product_tiles<DT, TA, TB, 128, 256, 1, Epi>(g, epi, most_split, st);
+    // fp32's parts need more than the one step that one stage holds
+    if (g.segs == 1) product_tiles<DT, TA, TB, 128, 256, 1, Epi>(g, epi, most_split, st);
+    else product_tiles<DT, TA, TB, 256, 256, 2, Epi>(g, epi, most_split, st);
+  } else if constexpr (TA) {
+    product_tiles<DT, TA, TB, 256, 64, 2, Epi>(g, epi, most_split, st);
+  } else if (g.n_real > kFewTokens) {
+    product_tiles<DT, TA, TB, 256, 256, 2, Epi>(g, epi, most_split, st);
+  } else if (few_tile_rows(g.m) == 128) {
+    product_tiles<DT, TA, TB, 128, 64, 2, Epi>(g, epi, most_split, st);
+  } else {
+    product_tiles<DT, TA, TB, 256, 64, 2, Epi>(g, epi, most_split, st);
   }
-  product_tiles<DT, TA, TB, 256, 256, 2, Epi>(g, epi, most_split, st);
 }
 
 template <int DT>
@@ -1497,40 +1536,46 @@ void grad_type(const Call& c, hipStream_t st) {
     product<DT, false, false>(g, ge, st);
     if (c.k > 0 && p.tokens > 0) entry_kernel<DT><<<(unsigned)p.tokens, 64, 0, st>>>(c, v0);
     // dhidden += g W: the inner index is the piece's vocabulary
-    if (c.dhidden != nullptr && p.tokens > 0) {
-      Product d{};
-      d.a = {w, p.piece * p.dimp, ldw, (int)p.dimp, (int)real};
-      d.b = {gbuf, p.rows * p.piece, p.piece, (int)p.rows, (int)p.piece};
-      d.m = (int)p.dimp;
-      d.n = (int)p.rows;
-      d.n_real = (int)p.tokens;
-      d.inner = round_up_int((int)real, 64);
-      d.live_n = true;
-      d.segs = g.segs;
-      d.split = true;
-      d.head = head;
-      SumEpi se{reinterpret_cast<float*>(c.ws + p.o_acc), p.dimp, (int)p.dimp,
-                v0 > 0};
-      product<DT, true, false>(d, se, st, p.acc_tiles);
-    }
+    Product d{};
+    d.a = {w, p.piece * p.dimp, ldw, (int)p.dimp, (int)real};
+    d.b = {gbuf, p.rows * p.piece, p.piece, (int)p.rows, (int)p.piece};
+    d.m = (int)p.dimp;
+    d.n = (int)p.rows;
+    d.n_real = (int)p.tokens;
+    d.inner = round_up_int((int)real, 64);
+    d.live_n = true;
+    d.segs = g.segs;
+    d.split = true;
+    d.head = head;
+    const SumEpi de{reinterpret_cast<float*>(c.ws + p.o_acc), p.dimp, (int)p.dimp, v0 > 0};
     // dweight of the piece: the inner index is the live rows
-    if (c.dweight != nullptr) {
-      Product d{};
-      d.a = {h, p.rows * p.dimp, p.dimp, (int)p.dimp, (int)p.rows};
-      d.b = {gbuf, p.rows * p.piece, p.piece, (int)p.piece, (int)p.rows};
-      d.m = (int)p.dimp;
-      d.n = (int)real;
-      d.inner = (int)p.rows;
-      d.inner_real = (int)p.tokens;
-      d.live_inner = true;
-      d.segs = g.segs;
-      d.head = head;
-      WeightEpi<DT> we{c.dweight, c.dweight_stride, v0, (int)p.dim,
-                       rows_aligned(c.dweight, c.dweight_stride, p.dtype, 8)   ? 8
-                       : rows_aligned(c.dweight, c.dweight_stride, p.dtype, 4) ? 4
-                                                                               : 1,
-                       head};
-      product<DT, true, true>(d, we, st);
+    Product e{};
+    e.a = {h, p.rows * p.dimp, p.dimp, (int)p.dimp, (int)p.rows};
+    e.b = {gbuf, p.rows * p.piece, p.piece, (int)p.piece, (int)p.rows};
+    e.m = (int)p.dimp;
+    e.n = (int)real;
+    e.inner = (int)p.rows;
+    e.inner_real = (int)p.tokens;
+    e.live_inner = true;
+    e.segs = g.segs;
+    e.head = head;
+    const WeightEpi<DT> we{c.dweight, c.dweight_stride, v0, (int)p.dim,
+                           rows_aligned(c.dweight, c.dweight_stride, p.dtype, 8)   ? 8
+                           : rows_aligned(c.dweight, c.dweight_stride, p.dtype, 4) ? 4
+                                                                                   : 1,
+                           head};
+    const bool want_d = c.dhidden != nullptr && p.tokens > 0, want_e = c.dweight != nullptr;
+    if (p.tokens > kFewTokens) {
+      const int64_t across = (p.dimp + 255) / 256;
+      const int64_t e_tiles = want_e ? (real + 255) / 256 * across : 0;
+      int64_t d_tiles = want_d ? p.rows / 256 * across : 0;
+      if (want_d && d_tiles < p.acc_tiles) d_tiles = p.acc_tiles;
+      const int first = (int)(e_tiles + 7) / 8 * 8;
+      gradients_kernel<DT><<<(unsigned)(first + (d_tiles + 7) / 8 * 8), 512, 0, st>>>(e, we, first,
+                                                                                   d, de);
+    } else {
+      if (want_d) product<DT, true, false>(d, de, st, p.acc_tiles);
+      if (want_e) product<DT, true, true>(e, we, st);
     }
   }
   if (c.dhidden != nullptr && p.tokens > 0)

@@ -84,7 +84,8 @@ zero_status check_head(const zero_head* h) {
 // last cache holds), or of packed weights. Smaller ones are taken where the rounds
 // of 256 tiles that the chip holds at once come out fuller, in all: the logits'
 // tiles [piece, tokens] take dim / 64 steps each, dweight's [dim, piece] tokens / 64,
-// either about four steps more, and a piece about eight in launches.
+// either about four steps more, and a piece about eight in launches. (dhidden's
+// tiles fill up dweight's last round.)
 int64_t choose_piece(const zloss::Plan& p, int64_t whole) {
   constexpr int64_t kPieceBytes = INT64_C(256) << 20;
   int64_t most = std::min<int64_t>(whole, INT64_C(1) << 21);
@@ -100,7 +101,9 @@ int64_t choose_piece(const zloss::Plan& p, int64_t whole) {
     for (int64_t v0 = 0; v0 < p.vocab; v0 += piece) {
       const int64_t m = ceil_div(std::min(piece, p.vocab - v0), 256);
       cost += 8 + ceil_div(m * (p.rows / 256), 256) * (p.dimp / 64 + 4);
-      if (p.grad) cost += ceil_div(m * ceil_div(p.dimp, 256), 256) * (p.rows / 64 + 4);
+      const int64_t across = ceil_div(p.dimp, 256);
+      if (p.grad)
+        cost += (m * across * (p.rows / 64 + 4) + p.rows / 256 * across * (m * 4 + 32)) / 256 + 16;
     }
     if (cost < best_cost) {
       best = piece;
