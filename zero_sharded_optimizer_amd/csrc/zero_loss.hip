@@ -251,8 +251,9 @@ __device__ __forceinline__ RowParam row_param(const Call& c, int64_t t, float sc
 }
 
 // dhidden has few tiles, [live, dim], and a long sum, over the piece's vocabulary,
-// which may be cut into runs. A tile takes its run's steps and about four more. Few
-// tokens: the number of runs with which the rounds of 512 tiles that the chip holds
+// which may be cut into runs. A tile takes its run's steps and, with the slab that is
+// written and read again, about sixteen more (taking four made 1600 live rows x
+// 65536 x 2048 4% slower, nothing faster). Few tokens: the number of runs with which the rounds of 512 tiles that the chip holds
 // at once end soonest. Else the tiles are started as dweight's of the same launch
 // end: `full` rounds of 256, and `rest` in one more; they are done at the first time
 // at which the units that were free from the start of that round, and those that
@@ -263,7 +264,7 @@ __device__ __forceinline__ int choose_splits(const Call& c, int live) {
   const int lane = threadIdx.x % 64, s = lane + 1, bn = few ? 64 : 256;
   const int across = (int)((p.dimp + 255) / 256);
   const int tiles = (live + bn - 1) / bn * across;
-  const int steps = ((int)(p.piece / 64) + s - 1) / s, each = steps + 4;
+  const int steps = ((int)(p.piece / 64) + s - 1) / s, each = steps + 16;
   int cost;
   if (few) {
     cost = (tiles * s + 511) / 512 * each;
@@ -415,7 +416,8 @@ __device__ __forceinline__ void pack8(const void* src, int64_t at, int k, int di
   }
 }
 
-// The live rows of hidden, zero rows up to the next multiple of kRowPad.
+// The live rows of hidden, zero rows up to the next multiple of kRowPad; for the
+// gradient the rows' parameters too.
 template <int DT>
 __global__ void __launch_bounds__(256) pack_hidden_kernel(Call c, bool wide) {
   const Plan& p = c.plan;
@@ -426,8 +428,14 @@ __global__ void __launch_bounds__(256) pack_hidden_kernel(Call c, bool wide) {
   u16* dst = reinterpret_cast<u16*>(c.ws + p.o_h) + (int64_t)r * p.dimp;
   const bool real = r < live;
   const float scale = DT == kF32 ? ldexpf(1.0f, scale_exponent(head->top_h)) : 1.0f;
-  const int64_t at =
-      real ? reinterpret_cast<const int*>(c.ws + p.o_rowmap)[r] * c.hidden_stride : 0;
+  const int64_t t = real ? reinterpret_cast<const int*>(c.ws + p.o_rowmap)[r] : 0;
+  const int64_t at = t * c.hidden_stride;
+  if (p.grad && threadIdx.x == 0) {
+    RowParam rp = {};
+    rp.target = -1;
+    if (real) rp = row_param(c, t, head->scale);
+    reinterpret_cast<RowParam*>(c.ws + p.o_rowp)[r] = rp;
+  }
   for (int k = threadIdx.x * 8; k < p.dimp; k += 256 * 8) {
     u32x4 v[kParts] = {};
     if (real) pack8<DT>(c.hidden, at, k, (int)p.dim, wide, scale, v);
@@ -849,8 +857,12 @@ struct Gather {
   const u16* w;     // the piece's weights
   int64_t ldw, v0;
   int real;
+  // Cross entropy takes few of the sixteen: the rows' first touch of a far page is
+  // what takes time, and more waves wait for more of them at once.
+  static constexpr int kRowsWave = 4;
   __host__ __device__ int64_t waves() const {
-    return c.k == 0 ? (c.plan.tokens + 15) / 16 : c.plan.tokens * ((c.k + 15) / 16);
+    return c.k == 0 ? (c.plan.tokens + kRowsWave - 1) / kRowsWave
+                    : c.plan.tokens * ((c.k + 15) / 16);
   }
   __device__ __forceinline__ void wave(int64_t id) const;
 };
@@ -861,11 +873,11 @@ __device__ __forceinline__ void Gather<DT>::wave(int64_t id) const {
   const int live = reinterpret_cast<const Head*>(c.ws + p.o_head)->live;
   const int K = c.k == 0 ? 1 : c.k, per_row = (K + 15) / 16;
   const int lane = threadIdx.x % 64, q = lane % 16;
-  const int row = (int)(c.k == 0 ? id * 16 + q : id / per_row);
+  const int row = (int)(c.k == 0 ? id * kRowsWave + q : id / per_row);
   const int k = c.k == 0 ? 0 : (int)(id % per_row) * 16 + q;
   int64_t m = -1;  // the pair's row in the piece
   int64_t t = 0;
-  if (row < live && k < K) {
+  if (row < live && k < K && (c.k != 0 || q < kRowsWave)) {
     t = reinterpret_cast<const int*>(c.ws + p.o_rowmap)[row];
     m = load_index(c.target, c.k == 0 ? t : t * c.index_stride + k, c.index64);
     m = m < 0 ? -1 : m - v0;  // padding has no weight row
@@ -881,17 +893,18 @@ __device__ __forceinline__ void Gather<DT>::wave(int64_t id) const {
   for (int seg = 0; seg < (DT == kF32 ? kSegs : 1); ++seg) {
     const u16* pa = a + (DT == kF32 ? seg_a(seg) * p.piece * p.dimp : 0);
     const u16* pb = h + (DT == kF32 ? seg_b(seg) * p.rows * p.dimp : 0);
-    for (int k0 = 0; k0 < p.dimp; k0 += 256) {  // eight loads on their way at a time
-      u32x4 va[8], vb[8];
+    constexpr int kDeep = 8;  // pairs of loads on their way at a time
+    for (int k0 = 0; k0 < p.dimp; k0 += kDeep * 32) {
+      u32x4 va[kDeep], vb[kDeep];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < kDeep; ++i) {
         int k = min(k0 + i * 32, (int)p.dimp - 32) + turn;
         k -= k >= p.dimp ? (int)p.dimp : 0;
         va[i] = *reinterpret_cast<const u32x4*>(pa + k);
         vb[i] = *reinterpret_cast<const u32x4*>(pb + k);
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int i = 0; i < kDeep; ++i)
         if (k0 + i * 32 < p.dimp) acc = mfma<DT>(va[i], vb[i], acc);
     }
   }
@@ -1303,18 +1316,6 @@ __global__ void __launch_bounds__(256) loss_kernel(Call c) {
 }
 
 // ---- Rows: the gradient -----------------------------------------------------
-__global__ void __launch_bounds__(256) row_param_kernel(Call c) {
-  const Plan& p = c.plan;
-  const Head* head = reinterpret_cast<const Head*>(c.ws + p.o_head);
-  const int64_t r = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (r >= round_up_int(head->live, (int)kRowPad)) return;
-  RowParam rp = {};
-  rp.target = -1;
-  if (r < head->live)
-    rp = row_param(c, reinterpret_cast<const int*>(c.ws + p.o_rowmap)[r], head->scale);
-  reinterpret_cast<RowParam*>(c.ws + p.o_rowp)[r] = rp;
-}
-
 // Distillation: g at the teacher's entries that lie in the piece, written over
 // what the tile left there: formed in one go from the saved logit, so that it
 // too is rounded once. One wave a live row.
@@ -1458,8 +1459,6 @@ void rows_and_hidden(const Call& c, hipStream_t st) {
   if (p.tokens > 0)
     pack_hidden_kernel<DT><<<(unsigned)p.rows, 256, 0, st>>>(
         c, rows_aligned(c.hidden, c.hidden_stride, p.dtype, 16 / (int)element(p.dtype)));
-  if (p.grad && p.tokens > 0)
-    row_param_kernel<<<(unsigned)((p.rows + 255) / 256), 256, 0, st>>>(c);
 }
 
 // The piece's weights as an operand source: packed, or where they are.
