@@ -947,13 +947,15 @@ __device__ __forceinline__ void turn_rows(lds_char* turn, const u32x2 (&part)[8]
   for (int i = 0; i < 8; ++i)
     *reinterpret_cast<lds_u32x2*>(turn + r * 256 + ((i * 2 + g / 2) ^ r) * 16 + g % 2 * 8) =
         part[i];
-  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  // (a wave's LDS instructions are carried out in their order: only the compiler is
+  // to be told)
+  asm volatile("" ::: "memory");
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     const int row = q * 4 + g;
     put(row, r, *reinterpret_cast<lds_u32x4*>(turn + row * 256 + (r ^ row) * 16));
   }
-  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  asm volatile("" ::: "memory");
 }
 
 template <int DT>
@@ -1047,10 +1049,13 @@ struct GradEpi {
     const int lane = threadIdx.x % 64;
     const float f = exponent_factor<DT>(head, inv_temp);
     const bool edge = m0 + MI * 16 > m_ext || n0 + NJ * 16 > n_ext;
+    RowParam rps[NJ];  // all loads on their way before the first is waited for
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) rps[j] = rows[n0 + j * 16 + lane % 16];
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
       const int n = n0 + j * 16 + lane % 16;
-      const RowParam rp = rows[n];
+      const RowParam& rp = rps[j];
       const int at = rp.target - m_base - m0 - lane / 16 * 4;  // 16 i + r where it is this lane's
 #pragma unroll
       for (int i = 0; i < MI; ++i)
@@ -1121,13 +1126,20 @@ struct SumEpi {
     for (int j = 0; j < NJ; ++j) {
       const int n = n0 + j * 16 + lane % 16;
       if (n >= n_ext) continue;
+      float* to = acc_out + ((int64_t)split * n_ext + n) * ld + m0 + lane / 16 * 4;
+      const int left = m_ext - m0 - lane / 16 * 4;
+      if (add) {
+        // eight loads at once: one after the other, each store's data would wait for its own
+        f32x4 old[MI];
 #pragma unroll
-      for (int i = 0; i < MI; ++i) {
-        const int m = m0 + i * 16 + lane / 16 * 4;
-        if (m >= m_ext) continue;
-        f32x4* o = reinterpret_cast<f32x4*>(acc_out + ((int64_t)split * n_ext + n) * ld + m);
-        *o = add ? *o + acc[i][j] : acc[i][j];
+        for (int i = 0; i < MI; ++i)
+          old[i] = *reinterpret_cast<const f32x4*>(to + (i * 16 < left ? i * 16 : 0));
+#pragma unroll
+        for (int i = 0; i < MI; ++i) acc[i][j] += old[i];
       }
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+        if (i * 16 < left) *reinterpret_cast<f32x4*>(to + i * 16) = acc[i][j];
     }
   }
 };
