@@ -39,6 +39,7 @@ workers sharing one GPU:
   zero_memory_bytes(...)                 -> per-rank memory by ZeRO stage
   zero_min_stage(n, N, mode, act, avail) -> the smallest stage that fits
   zero_shard_bounds(n, N, r)             -> np.array_split shard [a, b)
+The losses that make the gradients (include/zero_loss.h) are in .losses.
 """
 import ctypes as C
 from dataclasses import dataclass

@@ -8,6 +8,10 @@
 //   logits    [live, piece] = hidden W^T in tiles; the forward reduces each
 //             tile to softmax partials, the gradient turns it into g
 //   dhidden   += g W,   dweight = g^T hidden    (gradient, per piece)
+// The gradient makes the logits again: with the loss 8 operations for each token,
+// entry and dimension, in place of 6. Keeping them instead would be 4 bytes a logit
+// written and read again, the time of a product over some 1100 dimensions, and the
+// memory that the pieces are there to avoid.
 // Every product is one tiled kernel over 16-bit operands with fp32 sums. fp32
 // values go through it as two fp16 parts, x = hi + lo, each tensor scaled by the
 // power of two that brings its largest magnitude near 2^15: hi has 11 bits, lo
@@ -580,6 +584,20 @@ struct Product {
 // fall on different banks. The copy writes lane after lane, so the exchange is
 // made in the addresses it reads from. A transposed tile is turned by the
 // transposing LDS read, four inner steps of 16 rows a time.
+//
+// What bounds it. A 256 x 256 tile's step is 2048 cycles of matrix instructions on
+// each SIMD and takes some 2700: the matrix units are busy 74% of the time at 1.8
+// GHz, which is what the card's power allows at that load (a large library product
+// here has them busy 80% at 1.71 GHz, for 1.08 times the rate). 8192 x 131072 x 4096
+// makes its logits at 1.40 PFLOP/s; at 768 inner steps a tile's start and its
+// epilogue, which nothing overlaps, leave 0.97. Measured against it and slower:
+// four waves of 128 x 128 with the sums in accumulation registers (a third less LDS
+// reading, but nobody to work while a wave waits; 27.7 ms in place of 26.6 for the
+// whole of that case), a ring of five stages of 32 steps with a meeting each (27.1 in
+// place of 26.1: pieces of 64 bytes cost the copies more), blocks that stay and copy
+// their next tile during the epilogue (26.5 and 26.3: what the start costs is back in
+// registers spilled and rounds that no longer even out), copies issued in one go
+// instead of a few matrix instructions apart (27.6 and 26.2: they hold up the issue).
 typedef __attribute__((address_space(3))) char lds_char;
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
