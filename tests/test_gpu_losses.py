@@ -84,10 +84,13 @@ def test_xent_options(opt, dtype):
 
 @pytest.mark.parametrize("op", ["xent", "distill"])
 @pytest.mark.parametrize("dtype,T,V", [("fp32", 16385, 6001), ("bf16", 70000, 4500),
-                                       ("bf16", 70000, 4200), ("fp32", 1024, 50257)])
+                                       ("bf16", 70000, 4200), ("fp32", 1024, 50257),
+                                       ("fp16", 1000, 33001), ("bf16", 250, 40000),
+                                       ("fp32", 60, 40001)])
 def test_several_pieces(op, dtype, T, V):
     """More tokens than one piece of the whole vocabulary holds; last pieces that
-    end several tiles before the others do."""
+    end several tiles before the others do; and problems of one piece for each
+    width of the logits' tiles."""
     say(f"[case] {op} pieces {T} x {V} {dtype}")
     c = make(T, V, 64, dtype, seed=5, k=0 if op == "xent" else 7)
     c["up"] = c["up"] * 100

@@ -41,9 +41,6 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 // that is called instead of inlined puts them all into memory.
 #define INLINE __attribute__((always_inline))
 
-// Up to here the tiles are 64 columns wide.
-constexpr int kFewTokens = 64;
-
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // What the scan leaves for the kernels after it.
@@ -565,7 +562,6 @@ struct Operand {
 struct Product {
   Operand a, b;
   int m, n;        // extents (n: the most there can be, where live_n)
-  int n_real, inner_real;  // columns and inner steps that may mean something, at most
   int inner;       // inner extent, a multiple of 64 (the most there can be, where live_inner)
   bool live_n, live_inner;  // the extent is the live count, rounded up to 64 for the inner one
   bool split;      // the inner extent is cut into head->splits runs
@@ -612,14 +608,7 @@ struct Shape {
   static constexpr int kLds = STAGES * kStage;
 };
 
-// Few tokens: the weight's way from memory is all that counts. A vocabulary whose
-// tiles of 256 rows would leave half of the chip's compute units without one is cut
-// into tiles of 128: 32000 x 4096 takes 58 us in place of 67, while 50257 x 4096 and
-// more are faster in 256 (89 in place of 98).
-__host__ __device__ __forceinline__ int few_tile_rows(int vocab_rows) {
-  return (vocab_rows + 255) / 256 <= 128 ? 128 : 256;
-}
-// The inner step that such a tile, from vocabulary row m on, starts at.
+// The inner step that a narrow tile of the logits, from vocabulary row m on, starts at.
 __device__ __forceinline__ int first_step(int m, int tile_rows, int steps) {
   return m / tile_rows * 5 % steps;
 }
@@ -911,7 +900,7 @@ __device__ __forceinline__ void Gather<DT>::wave(int64_t id) const {
                  (int64_t)min(row, live - 1) * p.dimp + lane / 16 * 8;
   const u16* a = w + (mine ? m : 0) * ldw + lane / 16 * 8;
   // the narrow tiles' order of steps, each pair in that of its own weight row
-  const int turn = p.tokens <= kFewTokens && mine ? first_step((int)m, few_tile_rows(real), (int)p.dimp / 64) * 64 : 0;
+  const int turn = p.tile_n == 64 && mine ? first_step((int)m, p.tile_m, (int)p.dimp / 64) * 64 : 0;
   f32x4 acc = {};
   for (int seg = 0; seg < (DT == kF32 ? kSegs : 1); ++seg) {
     const u16* pa = a + (DT == kF32 ? seg_a(seg) * p.piece * p.dimp : 0);
@@ -1454,24 +1443,12 @@ void product_tiles(const Product& g, const Epi& epi, int64_t most_split, hipStre
       <<<(unsigned)((total + 7) / 8 * 8 + g.beside), Shape<BM, BN, STAGES>::kThreads, 0, st>>>(g, epi);
 }
 
-// Columns are tokens (few of them take narrower tiles) or, where the right
-// operand is transposed, vocabulary. (dhidden and dweight of more tokens share a
-// launch of their own.)
-template <int DT, bool TA, bool TB, class Epi>
-void product(const Product& g, const Epi& epi, hipStream_t st, int64_t most_split = 0) {
-  if constexpr (TB) {
-    // fp32's parts need more than the one step that one stage holds
-    if (g.segs == 1) product_tiles<DT, TA, TB, 128, 256, 1, Epi>(g, epi, most_split, st);
-    else product_tiles<DT, TA, TB, 256, 256, 2, Epi>(g, epi, most_split, st);
-  } else if constexpr (TA) {
-    product_tiles<DT, TA, TB, 256, 64, 2, Epi>(g, epi, most_split, st);
-  } else if (g.n_real > kFewTokens) {
-    product_tiles<DT, TA, TB, 256, 256, 2, Epi>(g, epi, most_split, st);
-  } else if (few_tile_rows(g.m) == 128) {
-    product_tiles<DT, TA, TB, 128, 64, 2, Epi>(g, epi, most_split, st);
-  } else {
-    product_tiles<DT, TA, TB, 256, 64, 2, Epi>(g, epi, most_split, st);
-  }
+// The logits, in the plan's tiles.
+template <int DT, class Epi>
+void logits(const Plan& p, const Product& g, const Epi& epi, hipStream_t st) {
+  if (p.tile_n == 256) product_tiles<DT, false, false, 256, 256, 2, Epi>(g, epi, 0, st);
+  else if (p.tile_m == 256) product_tiles<DT, false, false, 256, 64, 2, Epi>(g, epi, 0, st);
+  else product_tiles<DT, false, false, 128, 64, 2, Epi>(g, epi, 0, st);
 }
 
 template <int DT>
@@ -1521,7 +1498,6 @@ Product logits_product(const Call& c, const u16* w, int64_t ldw, int64_t real) {
          (int)p.dimp};
   g.m = (int)real;
   g.n = (int)p.rows;
-  g.n_real = (int)p.tokens;
   g.inner = (int)p.dimp;
   g.live_n = true;
   g.segs = DT == kF32 ? kSegs : 1;
@@ -1547,7 +1523,7 @@ void loss_type(const Call& c, hipStream_t st) {
     // Few tokens: the gather's few waves, which wait for memory ten times over, go
     // beside the tiles (8 to 13 us less). More would take the tiles' room in LDS.
     if (p.tokens <= kFewTokens) g.beside = (int)(pairs + 7) / 8 * 8;
-    product<DT, false, false>(g, epi, st);
+    logits<DT>(p, g, epi, st);
     if (p.tokens > kFewTokens)
       gather_kernel<DT><<<(unsigned)(blocks < (1 << 20) ? blocks : 1 << 20), 256, 0, st>>>(gather);
   }
@@ -1569,7 +1545,7 @@ void grad_type(const Call& c, hipStream_t st) {
     Product g = logits_product<DT>(c, w, ldw, real);
     GradEpi<DT> ge{head, reinterpret_cast<const RowParam*>(c.ws + p.o_rowp), gbuf, p.rows * p.piece,
                    p.piece, 1.0f / c.temperature, (int)v0, (int)real, c.smoothing != 0.0f};
-    product<DT, false, false>(g, ge, st);
+    logits<DT>(p, g, ge, st);
     if (c.k > 0 && p.tokens > 0) entry_kernel<DT><<<(unsigned)p.tokens, 64, 0, st>>>(c, v0);
     // dhidden += g W: the inner index is the piece's vocabulary
     Product d{};
@@ -1577,7 +1553,6 @@ void grad_type(const Call& c, hipStream_t st) {
     d.b = {gbuf, p.rows * p.piece, p.piece, (int)p.rows, (int)p.piece};
     d.m = (int)p.dimp;
     d.n = (int)p.rows;
-    d.n_real = (int)p.tokens;
     d.inner = round_up_int((int)real, 64);
     d.live_n = true;
     d.segs = g.segs;
@@ -1591,7 +1566,6 @@ void grad_type(const Call& c, hipStream_t st) {
     e.m = (int)p.dimp;
     e.n = (int)real;
     e.inner = (int)p.rows;
-    e.inner_real = (int)p.tokens;
     e.live_inner = true;
     e.segs = g.segs;
     e.head = head;
@@ -1610,8 +1584,11 @@ void grad_type(const Call& c, hipStream_t st) {
       gradients_kernel<DT><<<(unsigned)(first + (d_tiles + 7) / 8 * 8), 512, 0, st>>>(e, we, first,
                                                                                    d, de);
     } else {
-      if (want_d) product<DT, true, false>(d, de, st, p.acc_tiles);
-      if (want_e) product<DT, true, true>(e, we, st);
+      if (want_d) product_tiles<DT, true, false, 256, 64, 2>(d, de, p.acc_tiles, st);
+      // at most one inner step, and one stage: what counts is the result's way to
+      // memory. fp32's parts are more steps than one
+      if (want_e && DT != kF32) product_tiles<DT, true, true, 128, 256, 1>(e, we, 0, st);
+      if (want_e && DT == kF32) product_tiles<DT, true, true, 256, 256, 2>(e, we, 0, st);
     }
   }
   if (c.dhidden != nullptr && p.tokens > 0)

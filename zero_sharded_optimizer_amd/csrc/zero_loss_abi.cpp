@@ -115,6 +115,40 @@ int64_t choose_piece(const zloss::Plan& p, int64_t whole) {
   return best;
 }
 
+// The logits' tiles. A compute unit holds one of 256 x 256, two of 256 x 64 or three
+// of 128 x 64. The large one does most per byte it copies; the others are for
+// problems with fewer large tiles than the chip has units, and for few tokens, whose
+// logits are the weight's way from memory: more units read, and end together. Times
+// of a round of `held` tiles, and of a last one that gives each unit but one or two,
+// in microseconds a step and at the end, as measured (200 tokens x 5000 x 2048: 44, 29
+// and 24 us in this order; 200 x 32000 x 2048: 45, 40, 53; 500 x 32000 x 2048: 56, 74,
+// 88; 40 x 50257 x 4096: -, 72, 80).
+void choose_tile(zloss::Plan* p) {
+  struct Kind {
+    int m, n, held;
+    double step[3], more;  // by how many tiles the busiest unit has
+  };
+  static constexpr Kind kinds[3] = {{256, 256, 256, {1.35, 1.35, 1.35}, 6},
+                                    {256, 64, 512, {0.85, 1.15, 1.15}, 3},
+                                    {128, 64, 768, {0.70, 0.92, 1.05}, 3}};
+  const int64_t rows = std::min(p->piece, p->vocab);
+  const double steps = (double)(p->dimp / 64) * (p->planes > 1 ? 3 : 1);
+  double best = HUGE_VAL;
+  for (const Kind& k : kinds) {
+    if (k.n == 256 && p->tokens <= zloss::kFewTokens) continue;
+    const int64_t tiles = ceil_div(rows, k.m) * ceil_div(std::max<int64_t>(p->tokens, 1), k.n);
+    const int64_t full = tiles / k.held, rest = tiles % k.held;
+    const int last = k.held / 256 - 1;
+    double cost = (double)full * (k.step[last] * steps + k.more);
+    if (rest > 0) cost += k.step[std::min<int64_t>((rest - 1) / 256, last)] * steps + k.more;
+    if (cost < best) {
+      best = cost;
+      p->tile_m = k.m;
+      p->tile_n = k.n;
+    }
+  }
+}
+
 // The pieces and the workspace of one call.
 zloss::Plan make_plan(const zero_head& h, bool grad) {
   zloss::Plan p{};
@@ -135,10 +169,11 @@ zloss::Plan make_plan(const zero_head& h, bool grad) {
   // most 2^22 tiles (2^31 work-items, of the 2^32 that it could describe).
   p.piece = std::min(whole, (INT64_C(1) << 38) / p.rows / zloss::kVocPad * zloss::kVocPad);
   if (grad || p.pack_w) p.piece = choose_piece(p, whole);
+  choose_tile(&p);
   p.stat_cols = whole / zloss::kStatRows;
   // dhidden's sum over the vocabulary may be cut into slabs, as long as they are
   // at most this many tiles of 256 columns, and of 256 tokens or 64.
-  const int64_t tile_rows = h.tokens <= 64 ? 64 : 256;
+  const int64_t tile_rows = h.tokens <= zloss::kFewTokens ? 64 : 256;
   const int64_t tiles = ceil_div(std::max<int64_t>(h.tokens, 1), tile_rows) * ceil_div(p.dimp, 256);
   p.acc_tiles = (int)std::max<int64_t>(512, tiles);
 

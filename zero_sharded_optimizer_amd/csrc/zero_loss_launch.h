@@ -16,6 +16,8 @@ constexpr int64_t kVocPad = 256;  // vocabulary rows of a piece
 constexpr int64_t kDimPad = 64;   // the products' inner step
 // Vocabulary rows one entry of the softmax partials covers.
 constexpr int64_t kStatRows = 128;
+// Up to here the tiles of dhidden and dweight are made for few tokens.
+constexpr int kFewTokens = 64;
 
 // Sizes and workspace offsets of one call, made by the ABI layer.
 struct Plan {
@@ -27,6 +29,7 @@ struct Plan {
   int64_t rows;      // tokens padded to kRowPad
   int64_t dimp;      // dim padded to kDimPad
   int64_t piece;     // vocabulary rows per piece, a multiple of kVocPad
+  int tile_m, tile_n; // the logits' tiles: vocabulary rows (256 or 128), tokens (256 or 64)
   int64_t stat_cols; // softmax partials per token
   int acc_tiles;     // tiles that the slabs of dhidden's sum have room for
   // workspace offsets, bytes
