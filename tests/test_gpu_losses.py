@@ -375,3 +375,39 @@ def test_example_learns(precision):
     say("  ", first, last)
     for name in first:
         assert math.isfinite(last[name]) and last[name] < first[name] / 2, (first, last)
+
+
+def test_weight_of_more_than_2_to_the_31_elements():
+    """Offsets beyond 32 bits in the weight and its gradient, targets at both ends."""
+    say("[case] 530000 x 4096")
+    V, D, T = 530000, 4096, 5
+    w = torch.empty(V, D, dtype=torch.bfloat16, device="cuda")
+    w.normal_(0.0, 1.5 / math.sqrt(D), generator=torch.Generator("cuda").manual_seed(23))
+    h = torch.randn(T, D, generator=torch.Generator().manual_seed(24)).bfloat16().cuda()
+    c = {"hidden": h, "weight": w, "up": torch.full((T,), 0.2, device="cuda"),
+         "target": torch.tensor([V - 1, 0, V // 2, -100, V - 129]).cuda()}
+    loss, saved, dh, dw = run(c, {})
+    # the same rows in small pieces: only the sums over the vocabulary join them
+    z = torch.cat([h.double() @ x.double().T for x in w.split(1 << 16)], 1)
+    lse = torch.logsumexp(z, 1)
+    live = c["target"] >= 0
+    g = torch.softmax(z, 1) * 0.2 * live[:, None]
+    rows = torch.nonzero(live)[:, 0]
+    g[rows, c["target"][rows]] -= 0.2
+    want = torch.where(live, lse - z[torch.arange(T), c["target"].clamp(min=0)], 0.0)
+    # |z| < 10, each off by (D + 16) 2^-24 of sum|h||w| < 70; the sum as in loss_cases
+    assert float((loss - want).abs().max()) <= 2 * (D + 16) * 2.0 ** -24 * 70 \
+        + (V / 64 + 200) * 2.0 ** -24
+    u, slack = 2.0 ** -8, 2 * (D + V / 64 + 300) * 2.0 ** -24 * 70
+    at = 0
+    r_dh = torch.zeros(T, D, dtype=torch.float64, device="cuda")
+    b_dh = torch.zeros_like(r_dh)
+    for x, gx in zip(w.split(1 << 16), g.split(1 << 16, dim=1)):
+        r_dh += gx @ x.double()
+        b_dh += gx.abs() @ x.double().abs()
+        r_dw, b_dw = gx.T @ h.double(), gx.T.abs() @ h.double().abs()
+        d = (dw[at:at + x.shape[0]].double() - r_dw).abs()
+        assert bool((d <= u * r_dw.abs() + (u * (1 + u) + slack) * b_dw + 1e-37).all()), at
+        at += x.shape[0]
+    d = (dh.double() - r_dh).abs()
+    assert bool((d <= u * r_dh.abs() + (u * (1 + u) + slack + V * 2.0 ** -24) * b_dh).all())

@@ -582,7 +582,7 @@ struct Product {
 // transposing LDS read, four inner steps of 16 rows a time.
 //
 // What bounds it. A 256 x 256 tile's step is 2048 cycles of matrix instructions on
-// each SIMD and takes some 2700: the matrix units are busy 74% of the time at 1.8
+// each SIMD and takes some 2700: the matrix units are busy 77% of the time at 1.82
 // GHz, which is what the card's power allows at that load (a large library product
 // here has them busy 80% at 1.71 GHz, for 1.08 times the rate). 8192 x 131072 x 4096
 // makes its logits at 1.40 PFLOP/s; at 768 inner steps a tile's start and its
