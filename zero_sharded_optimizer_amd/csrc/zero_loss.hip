@@ -1350,8 +1350,12 @@ __global__ void __launch_bounds__(64) entry_kernel(Call c, int64_t v0) {
   const Plan& p = c.plan;
   const int r = blockIdx.x, lane = threadIdx.x;
   if (r >= reinterpret_cast<const Head*>(c.ws + p.o_head)->live) return;
-  __shared__ int idx[1024];
-  __shared__ float pk[1024];
+  __shared__ int idx[1024 + 8];
+  __shared__ float pk[1024 + 8];
+  if (lane < 8) {  // the search below goes by eights
+    idx[c.k + lane] = -2;
+    pk[c.k + lane] = 0.0f;
+  }
   const int64_t t = reinterpret_cast<const int*>(c.ws + p.o_rowmap)[r];
   const RowParam rp = reinterpret_cast<const RowParam*>(c.ws + p.o_rowp)[r];
   const float inv_temp = 1.0f / c.temperature;
@@ -1377,9 +1381,12 @@ __global__ void __launch_bounds__(64) entry_kernel(Call c, int64_t v0) {
   for (int k = lane; k < c.k; k += 64) {
     const int64_t m = idx[k] - v0;
     if (idx[k] < 0 || m < 0 || m >= p.piece) continue;
-    float same = 0.0f;
-    for (int q = 0; q < c.k; ++q) same += idx[q] == idx[k] ? pk[q] : 0.0f;
     const float z = c.logit_in[t * c.k + k] * inv_temp;
+    const int own = idx[k];
+    float same = 0.0f;
+    for (int q = 0; q < c.k; q += 8)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) same += idx[q + e] == own ? pk[q + e] : 0.0f;
     const float x = rp.a * (exp_f(z - rp.lse) - same / total);
     if constexpr (DT == kF32) {
       u16 parts[kParts];
