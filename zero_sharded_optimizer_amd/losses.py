@@ -30,7 +30,9 @@ worker's flat gradient buffer, where the sharded step reads them:
     dh, _ = linear_xent_grad(h, weight, target, saved, 1.0 / n, dweight=head)
     h.backward(dh)                                  # the rest of the model
 
-hidden, weight and their gradients are bf16, fp16 or fp32, all alike. This
+hidden, weight and their gradients are bf16, fp16 or fp32, all alike. Work is
+enqueued on `stream` (torch's current one by default) and outputs are allocated
+for it; inputs from another stream are the caller's to order, and to record. This
 module checks and marshals arguments and allocates outputs and workspace from
 torch; every step of the computation runs in libzero.so's HIP kernels.
 """
@@ -187,6 +189,17 @@ def _on_stream(stream, hidden):
     return torch.cuda.stream(stream)  # also makes its device the current one
 
 
+def _handle(stream, like):
+    """The stream's hipStream_t. torch's current one is asked for directly where
+    torch offers that: a Stream object takes 5 us to make."""
+    if stream is None:
+        import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None:
+            return raw(like.device.index)
+    return _stream_handle(stream, like)
+
+
 def _workspace(head, want_grad, workspace, like):
     import torch
     need = _workspace_bytes(head, want_grad)
@@ -212,7 +225,7 @@ def linear_xent(hidden, weight, target, ignore_index: int = -100, label_smoothin
         ws, nbytes = _workspace(head, False, workspace, hidden)
         st = lib.zero_linear_xent(C.byref(head), C.byref(params), loss.data_ptr() or None,
                                   lse.data_ptr() or None, ws.data_ptr(), nbytes,
-                                  _stream_handle(stream, hidden))
+                                  _handle(stream, hidden))
     if st != _abi.ZERO_OK:
         _raise(st)
     return loss, Saved(lse)
@@ -234,7 +247,7 @@ def linear_distill(hidden, weight, index, logit, temperature: float = 1.0, works
         ws, nbytes = _workspace(head, False, workspace, hidden)
         st = lib.zero_linear_distill(C.byref(head), C.byref(params), loss.data_ptr() or None,
                                      lse.data_ptr() or None, kept.data_ptr() or None,
-                                     ws.data_ptr(), nbytes, _stream_handle(stream, hidden))
+                                     ws.data_ptr(), nbytes, _handle(stream, hidden))
     if st != _abi.ZERO_OK:
         _raise(st)
     return loss, Saved(lse, kept)
@@ -292,7 +305,7 @@ def _grad(entry, hidden, weight, head, params, saved, extra, upstream, dhidden, 
             return dhidden, None  # no row: nothing is written
         ws, nbytes = _workspace(head, True, workspace, hidden)
         st = entry(C.byref(head), C.byref(params), saved.lse.data_ptr() or None, *extra,
-                   C.byref(g), ws.data_ptr(), nbytes, _stream_handle(stream, hidden))
+                   C.byref(g), ws.data_ptr(), nbytes, _handle(stream, hidden))
     if st != _abi.ZERO_OK:
         _raise(st)
     return dhidden if need_dhidden else None, dweight if need_dweight else None
