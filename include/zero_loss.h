@@ -31,12 +31,14 @@
  * units; softmax statistics, losses and the sum over the vocabulary of dhidden
  * in fp32. g is rounded once to the given type for its products (bf16; fp16
  * after a scaling that keeps the largest |u_t| near 2^14, undone in fp32 before
- * the result is rounded). In fp32 hidden, weight and g are each
- * held as two fp16 parts under a power-of-two scale of their own, and three of
- * the four part products are summed: 24 bits for values above 2^-17 of the
- * tensor's largest magnitude (for g: of the largest |u_t|), an absolute 2^-40 of
- * that magnitude below. The same call gives the same bits: nothing is summed in
- * an order left to chance.
+ * the result is rounded). In fp32 hidden, weight and g are each held as two
+ * fp16 parts under a power-of-two scale of their own, and three of the four
+ * part products are summed: 24 bits for values above 2^-17 of the tensor's
+ * largest magnitude (for g: of the largest |u_t|), an absolute 2^-40 of that
+ * magnitude below. Largest is among the finite: an infinity or a NaN in one row
+ * leaves the other rows as they are; in fp32 a product with an infinity may be
+ * NaN where it would otherwise be infinite. The same call gives the same bits:
+ * nothing is summed in an order left to chance.
  *
  * Conventions are those of zero_adam.h: caller-owned device buffers, work
  * enqueued on `stream`, arguments validated before any HIP call, status codes,

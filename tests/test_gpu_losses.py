@@ -122,6 +122,40 @@ def test_empty_rows_may_hold_anything(op, dtype):
     assert (dh[at] == 0).all() and (saved.lse[at] == 0).all()
 
 
+@pytest.mark.parametrize("what", ["hidden", "upstream"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("op", ["xent", "distill"])
+@pytest.mark.parametrize("tokens", [29, 77])
+@pytest.mark.parametrize("dtype", list(DTYPES))
+def test_a_live_row_that_is_not_finite_leaves_the_others(dtype, tokens, op, bad, what):
+    """One element of one live row: the other rows' losses and dhidden stand as
+    without it, at a scale of hidden and upstream that needs the operands' own."""
+    say(f"[case] {op} {bad} in a live row's {what} {dtype} {tokens}")
+    c = make(tokens, 300, 64, dtype, seed=12, k=0 if op == "xent" else 4)
+    shift = 13 if dtype == "fp32" else 4
+    c["hidden"] *= 2.0 ** -shift
+    c["weight"] *= 2.0 ** shift
+    c["up"] *= 2.0 ** -10
+    live = c["target"] != -100 if op == "xent" else (c["index"] >= 0).any(1)
+    row = int(torch.nonzero(live)[5, 0])
+    opt = {"z_loss": 1e-3} if op == "xent" else {"temperature": 2.0}
+    plain = {k: v.clone() for k, v in c.items()}
+    plain["up"][row] = 0.0
+    if what == "hidden":
+        c["hidden"][row, 40] = bad
+    else:
+        c["up"][row] = bad
+    loss, saved, dh, dw = run(c, opt)
+    r_loss, r_lse, r_dh, _, b = reference(plain, **opt)
+    keep = torch.arange(tokens, device="cuda") != row
+    check("loss", loss[keep], r_loss[keep], b["loss"][keep])
+    check("lse", saved.lse[keep], r_lse[keep], b["lse"][keep])
+    check("dhidden", dh[keep], r_dh[keep], b["dh"][keep])
+    assert not torch.isfinite(dh[row]).any() and not torch.isfinite(dw).all()
+    if what == "hidden":
+        assert not torch.isfinite(loss[row])
+
+
 @pytest.mark.parametrize("op", ["xent", "distill"])
 def test_no_live_row(op):
     say(f"[case] {op} no live row")

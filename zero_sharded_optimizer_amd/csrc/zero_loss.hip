@@ -49,15 +49,15 @@ struct Head {
   int splits;       // runs that dhidden's sum over a piece of the vocabulary is cut into
   float scale;      // what g is held at
   float inv_scale;
-  // fp32: the bits of the largest magnitude in the live rows of hidden, and in the
-  // weight. (Non-negative floats order as their bits do, NaN above all.)
+  // fp32: the bits of the largest finite magnitude in the live rows of hidden, and in
+  // the weight. (Non-negative floats order as their bits do, infinity and NaN above all.)
   uint32_t top_h, top_w;
 };
 
-// The power of two that brings `top` to [2^14, 2^15), within 2^+-100, and 1 for
-// zero, infinities and NaN.
+// The power of two that brings the finite `top` to [2^14, 2^15), within 2^+-100, and
+// 1 for zero.
 __device__ __forceinline__ int scale_exponent(float top) {
-  if (!(top > 0.0f && top < INFINITY)) return 0;
+  if (top == 0.0f) return 0;
   const int e = 14 - ilogbf(top);
   return e < -100 ? -100 : e > 100 ? 100 : e;
 }
@@ -212,13 +212,15 @@ __global__ void __launch_bounds__(256) classify_kernel(Call c, uint8_t* state) {
 }
 
 // The largest |g| a row can have, and the size of its pull on its target (short of
-// the smoothing, which all rows share).
+// the smoothing, which all rows share). A row whose g cannot be finite has no say in
+// the scale that the others share.
 struct Reach {
   float top, pull;
 };
 __device__ __forceinline__ Reach row_reach(const Call& c, int64_t t) {
   const float u = fabsf(c.upstream[t * c.upstream_stride]) * c.temperature;
-  return {c.z_loss != 0.0f ? u * (1.0f + 2.0f * c.z_loss * fabsf(c.lse_in[t])) : u, u};
+  const float top = c.z_loss != 0.0f ? u * (1.0f + 2.0f * c.z_loss * fabsf(c.lse_in[t])) : u;
+  return top < INFINITY ? Reach{top, u} : Reach{0.0f, 0.0f};
 }
 
 // The scale that g is held at. The largest |g| a row can have comes to (2^13,
@@ -348,11 +350,16 @@ __global__ void __launch_bounds__(1024) scan_kernel(Call c) {
 }
 
 // ---- Packing --------------------------------------------------------------
-// fp32: the largest magnitudes of the weight and, in the last kTopHidden blocks,
-// of the live rows of hidden. The largest of largest in any order is the same
+// fp32: the largest finite magnitudes of the weight and, in the last kTopHidden
+// blocks, of the live rows of hidden: what is not finite stays so under any scale,
+// and must not choose one for the rows beside it. The largest of largest in any order is the same
 // number, so the atomics leave nothing to chance; there is one a block, since
 // they all wait for each other (one a wave: 165 us in place of 40 for 154 MB).
 constexpr int kTopHidden = 64, kTopBlocks = 1024;
+__device__ __forceinline__ uint32_t finite_size(uint32_t bits) {
+  bits &= 0x7fffffffu;
+  return bits < 0x7f800000u ? bits : 0;
+}
 __global__ void __launch_bounds__(256) top_kernel(Call c, bool wide_h, bool wide_w) {
   const Plan& p = c.plan;
   Head* head = reinterpret_cast<Head*>(c.ws + p.o_head);
@@ -370,9 +377,9 @@ __global__ void __launch_bounds__(256) top_kernel(Call c, bool wide_h, bool wide
     for (int k = lane * 4; k < bulk; k += 256) {
       const u32x4 v = *reinterpret_cast<const u32x4*>(x + k);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) top = max(top, v[i] & 0x7fffffffu);
+      for (int i = 0; i < 4; ++i) top = max(top, finite_size(v[i]));
     }
-    for (int k = bulk + lane; k < p.dim; k += 64) top = max(top, x[k] & 0x7fffffffu);
+    for (int k = bulk + lane; k < p.dim; k += 64) top = max(top, finite_size(x[k]));
   }
 #pragma unroll
   for (int d = 32; d; d >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
