@@ -82,8 +82,8 @@ typedef struct {
   int32_t index_dtype;    /* a zero_index_dtype: of target */
   int32_t reserved;       /* must be 0 */
   int64_t ignore_index;   /* a target of this value makes its row empty */
-  double label_smoothing; /* in [0, 1) */
-  double z_loss;          /* finite, >= 0 */
+  double label_smoothing; /* in [0, 1), as a float */
+  double z_loss;          /* finite as a float, >= 0 */
 } zero_xent_params;
 
 /* A teacher's top-K entries. index < 0 is padding, and so is a logit of -inf.

@@ -92,7 +92,9 @@ def test_head_refusals(kw, words):
     (dict(index_dtype=2), "index_dtype"), (dict(label_smoothing=1.0), "label_smoothing"),
     (dict(label_smoothing=-0.1), "label_smoothing"),
     (dict(label_smoothing=math.nan), "label_smoothing"), (dict(z_loss=-1.0), "z_loss"),
-    (dict(z_loss=math.inf), "z_loss"), (dict(reserved=1), "reserved")], ids=str)
+    (dict(z_loss=math.inf), "z_loss"), (dict(z_loss=1e39), "z_loss"),
+    (dict(label_smoothing=1.0 - 2.0 ** -40), "label_smoothing"),
+    (dict(reserved=1), "reserved")], ids=str)
 def test_xent_refusals(kw, words):
     refused(call_xent(head(), xent(**kw)), words)
     refused(call_xent_grad(head(), xent(**kw), grads()), words)

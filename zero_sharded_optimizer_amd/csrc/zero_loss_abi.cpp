@@ -258,10 +258,10 @@ zero_status check_xent(const zero_head& h, const zero_xent_params* p) {
   if (p->target == nullptr && h.tokens > 0) return fail(ZERO_EINVAL, "target is NULL");
   if (!aligned(p->target, (uintptr_t)index_size(p->index_dtype)))
     return fail(ZERO_EINVAL, "target must be aligned to its element size");
-  if (!(p->label_smoothing >= 0.0 && p->label_smoothing < 1.0))
-    return fail(ZERO_EINVAL, "label_smoothing must be in [0, 1)");
-  if (!(std::isfinite(p->z_loss) && p->z_loss >= 0.0))
-    return fail(ZERO_EINVAL, "z_loss must be finite and >= 0");
+  if (!(p->label_smoothing >= 0.0 && (float)p->label_smoothing < 1.0f))
+    return fail(ZERO_EINVAL, "label_smoothing must be in [0, 1) (as a float)");
+  if (!(std::isfinite((float)p->z_loss) && p->z_loss >= 0.0))
+    return fail(ZERO_EINVAL, "z_loss must be finite (as a float) and >= 0");
   return ZERO_OK;
 }
 
