@@ -352,42 +352,56 @@ __global__ void __launch_bounds__(1024) scan_kernel(Call c) {
 // ---- Packing --------------------------------------------------------------
 // fp32: the largest finite magnitudes of the weight and, in the last kTopHidden
 // blocks, of the live rows of hidden: what is not finite stays so under any scale,
-// and must not choose one for the rows beside it. The largest of largest in any order is the same
-// number, so the atomics leave nothing to chance; there is one a block, since
-// they all wait for each other (one a wave: 165 us in place of 40 for 154 MB).
-constexpr int kTopHidden = 64, kTopBlocks = 1024;
+// and must not choose one for the rows beside it. The largest of largest in any
+// order is the same number, so the atomics leave nothing to chance; there is one a
+// block of sixteen waves, since they all wait for each other (for 154 MB, one a wave
+// took 165 us, one every four waves 37 us, this 29 us). A wave reads kTopRows rows at
+// once, to have their loads in flight together.
+constexpr int kTopHidden = 16, kTopBlocks = 512, kTopRows = 4;
 __device__ __forceinline__ uint32_t finite_size(uint32_t bits) {
   bits &= 0x7fffffffu;
   return bits < 0x7f800000u ? bits : 0;
 }
-__global__ void __launch_bounds__(256) top_kernel(Call c, bool wide_h, bool wide_w) {
+__global__ void __launch_bounds__(1024) top_kernel(Call c, bool wide_h, bool wide_w) {
   const Plan& p = c.plan;
   Head* head = reinterpret_cast<Head*>(c.ws + p.o_head);
   const int first_h = (int)gridDim.x - kTopHidden;
   const bool is_h = (int)blockIdx.x >= first_h, wide = is_h ? wide_h : wide_w;
   const int64_t rows = is_h ? head->live : p.vocab, pitch = is_h ? c.hidden_stride : c.weight_stride;
   const int wave = threadIdx.x / 64, lane = threadIdx.x % 64;
-  const int64_t first = ((int)blockIdx.x - (is_h ? first_h : 0)) * 4 + wave;
-  const int64_t step = (is_h ? kTopHidden : first_h) * 4;
+  const int64_t first = ((int)blockIdx.x - (is_h ? first_h : 0)) * 16 + wave;
+  const int64_t step = (is_h ? kTopHidden : first_h) * 16;
   uint32_t top = 0;
-  for (int64_t r = first; r < rows; r += step) {
-    const int64_t row = is_h ? reinterpret_cast<const int*>(c.ws + p.o_rowmap)[r] : r;
-    const uint32_t* x = static_cast<const uint32_t*>(is_h ? c.hidden : c.weight) + row * pitch;
+  for (int64_t r = first; r < rows; r += kTopRows * step) {
+    const uint32_t* x[kTopRows];  // beyond the last row: the last once more
+#pragma unroll
+    for (int j = 0; j < kTopRows; ++j) {
+      const int64_t at = min(r + j * step, rows - 1);
+      const int64_t row = is_h ? reinterpret_cast<const int*>(c.ws + p.o_rowmap)[at] : at;
+      x[j] = static_cast<const uint32_t*>(is_h ? c.hidden : c.weight) + row * pitch;
+    }
     const int bulk = wide ? (int)p.dim / 4 * 4 : 0;
     for (int k = lane * 4; k < bulk; k += 256) {
-      const u32x4 v = *reinterpret_cast<const u32x4*>(x + k);
+      u32x4 v[kTopRows];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) top = max(top, finite_size(v[i]));
+      for (int j = 0; j < kTopRows; ++j) v[j] = *reinterpret_cast<const u32x4*>(x[j] + k);
+#pragma unroll
+      for (int j = 0; j < kTopRows; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = max(top, finite_size(v[j][i]));
     }
-    for (int k = bulk + lane; k < p.dim; k += 64) top = max(top, finite_size(x[k]));
+    for (int k = bulk + lane; k < p.dim; k += 64)
+#pragma unroll
+      for (int j = 0; j < kTopRows; ++j) top = max(top, finite_size(x[j][k]));
   }
 #pragma unroll
   for (int d = 32; d; d >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
-  __shared__ uint32_t tops[4];
+  __shared__ uint32_t tops[16];
   if (lane == 0) tops[wave] = top;
   __syncthreads();
   if (threadIdx.x == 0) {
-    top = max(max(tops[0], tops[1]), max(tops[2], tops[3]));
+#pragma unroll
+    for (int i = 1; i < 16; ++i) top = max(top, tops[i]);
     if (top != 0) atomicMax(is_h ? &head->top_h : &head->top_w, top);
   }
 }
@@ -1478,9 +1492,9 @@ void rows_and_hidden(const Call& c, hipStream_t st) {
         c, reinterpret_cast<uint8_t*>(c.ws + p.o_state));
   scan_kernel<<<1, 1024, 0, st>>>(c);
   if (DT == kF32) {
-    const int64_t w_blocks = (p.vocab + 3) / 4;
+    const int64_t w_blocks = (p.vocab + 16 * kTopRows - 1) / (16 * kTopRows);
     const int blocks = (int)(w_blocks < kTopBlocks ? w_blocks : kTopBlocks) + kTopHidden;
-    top_kernel<<<blocks, 256, 0, st>>>(
+    top_kernel<<<blocks, 1024, 0, st>>>(
         c, rows_aligned(c.hidden, c.hidden_stride, p.dtype, 4),
         rows_aligned(c.weight, c.weight_stride, p.dtype, 4));
   }
