@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(1024) scan_kernel(Call c) {
 // and must not choose one for the rows beside it. The largest of largest in any
 // order is the same number, so the atomics leave nothing to chance; there is one a
 // block of sixteen waves, since they all wait for each other (for 154 MB, one a wave
-// took 165 us, one every four waves 37 us, this 29 us). A wave reads kTopRows rows at
+// took 165 us, one every four waves 38 us, this 31 us). A wave reads kTopRows rows at
 // once, to have their loads in flight together.
 constexpr int kTopHidden = 16, kTopBlocks = 512, kTopRows = 4;
 __device__ __forceinline__ uint32_t finite_size(uint32_t bits) {
