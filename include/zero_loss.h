@@ -29,7 +29,9 @@
  *
  * Arithmetic: products of the given types' values with fp32 sums on the matrix
  * units; softmax statistics, losses and the sum over the vocabulary of dhidden
- * in fp32. g is rounded once to the given type for its products (bf16; fp16
+ * in fp32. loss and lse are rounded by the size of the row's largest logit over the
+ * temperature, and so is what a probability in the gradient is formed from (beyond
+ * some 2^20 that is more than the difference of neighbours). g is rounded once to the given type for its products (bf16; fp16
  * after a scaling that keeps the largest |u_t| near 2^14, undone in fp32 before
  * the result is rounded). In fp32 hidden, weight and g are each held as two
  * fp16 parts under a power-of-two scale of their own, and three of the four

@@ -156,6 +156,12 @@ __device__ __forceinline__ float exp_f(float x) { return __builtin_amdgcn_exp2f(
 // that an exponent of two relative to it is rounded once, by its own size.
 __device__ __forceinline__ float sixteenths(float x) { return rintf(x * 16.0f) * 0.0625f; }
 
+// From here on fp32 has no sixteenths. A base may then be off by more than the exponents
+// of two that are normal, and what is relative to it infinite: exponents are taken from
+// the largest logit itself, or held to what a probability can have, and the base's own
+// rounding, as large as the logits', is let go.
+constexpr float kHugeBase = 0x1p20f;
+
 template <int DT>
 __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
   if constexpr (DT != kBF16)
@@ -255,7 +261,7 @@ __device__ __forceinline__ RowParam row_param(const Call& c, int64_t t, float sc
   }
   const double l2 = rp.lse * 1.4426950408889634;
   rp.base = sixteenths((float)l2);
-  rp.a2 = (float)(rp.a * exp2(rp.base - l2));
+  rp.a2 = fabsf(rp.base) >= kHugeBase ? rp.a : (float)(rp.a * exp2(rp.base - l2));
   return rp;
 }
 
@@ -1043,11 +1049,22 @@ struct StatEpi {
       top = fmaxf(top, __shfl_xor(top, 16));
       top = fmaxf(top, __shfl_xor(top, 32));
       const float base = top == -INFINITY ? 0.0f : sixteenths(top * f);
+      const bool huge = fabsf(base) >= kHugeBase;
+      if (!__any(huge)) {
 #pragma unroll
-      for (int i = 0; i < MI; ++i)
+        for (int i = 0; i < MI; ++i)
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          total += __builtin_amdgcn_exp2f(fmaf(acc[i][j][r], f, -base));
+          for (int r = 0; r < 4; ++r)
+            total += __builtin_amdgcn_exp2f(fmaf(acc[i][j][r], f, -base));
+      } else {
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float x = acc[i][j][r];
+            total += __builtin_amdgcn_exp2f(huge ? (x - top) * f : fmaf(x, f, -base));
+          }
+      }
       total += __shfl_xor(total, 16);
       total += __shfl_xor(total, 32);
       const int n = n0 + j * 16 + lane % 16;
@@ -1092,11 +1109,22 @@ struct GradEpi {
       const int n = n0 + j * 16 + lane % 16;
       const RowParam& rp = rps[j];
       const int at = rp.target - m_base - m0 - lane / 16 * 4;  // 16 i + r where it is this lane's
+      const bool huge = fabsf(rp.base) >= kHugeBase;
+      if (!__any(huge)) {
 #pragma unroll
-      for (int i = 0; i < MI; ++i)
+        for (int i = 0; i < MI; ++i)
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          acc[i][j][r] = rp.a2 * __builtin_amdgcn_exp2f(fmaf(acc[i][j][r], f, -rp.base));
+          for (int r = 0; r < 4; ++r)
+            acc[i][j][r] = rp.a2 * __builtin_amdgcn_exp2f(fmaf(acc[i][j][r], f, -rp.base));
+      } else {
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float x = fmaf(acc[i][j][r], f, -rp.base);
+            acc[i][j][r] = rp.a2 * __builtin_amdgcn_exp2f(huge && x > 0.0f ? 0.0f : x);
+          }
+      }
       if (shift) {
 #pragma unroll
         for (int i = 0; i < MI; ++i) acc[i][j] -= rp.c;
@@ -1410,7 +1438,8 @@ __global__ void __launch_bounds__(64) entry_kernel(Call c, int64_t v0) {
     for (int q = 0; q < c.k; q += 8)
 #pragma unroll
       for (int e = 0; e < 8; ++e) same += idx[q + e] == own ? pk[q + e] : 0.0f;
-    const float x = rp.a * (exp_f(z - rp.lse) - same / total);
+    const float below = z - rp.lse;  // above only by rounding
+    const float x = rp.a * (exp_f(below > 0.0f ? 0.0f : below) - same / total);
     if constexpr (DT == kF32) {
       u16 parts[kParts];
       split2(x, parts);
