@@ -33,14 +33,12 @@
  * temperature, and so is what a probability in the gradient is formed from (beyond
  * some 2^20 that is more than the difference of neighbours). g is rounded once to the given type for its products (bf16; fp16
  * after a scaling that keeps the largest |u_t| near 2^14, undone in fp32 before
- * the result is rounded). In fp32 hidden, weight and g are each held as two
- * fp16 parts under a power-of-two scale of their own, and three of the four
- * part products are summed: 24 bits for values above 2^-17 of the tensor's
- * largest magnitude (for g: of the largest |u_t|), an absolute 2^-40 of that
- * magnitude below. Largest is among the finite: an infinity or a NaN in one row
- * leaves the other rows as they are; in fp32 a product with an infinity may be
- * NaN where it would otherwise be infinite. The same call gives the same bits:
- * nothing is summed in an order left to chance.
+ * the result is rounded). In fp32 hidden, weight and g are each held as three bf16
+ * parts, all 24 bits of every value, and six of the nine part products are summed:
+ * what is left out is below 2^-23 of each product. A row with an infinity or a NaN
+ * leaves the other rows' losses and dhidden as they are; in fp32 a product with an
+ * infinity may be NaN where it would otherwise be infinite. The same call gives the
+ * same bits: nothing is summed in an order left to chance.
  *
  * Conventions are those of zero_adam.h: caller-owned device buffers, work
  * enqueued on `stream`, arguments validated before any HIP call, status codes,

@@ -13,13 +13,13 @@
 // written and read again, the time of a product over some 1100 dimensions, and the
 // memory that the pieces are there to avoid.
 // Every product is one tiled kernel over 16-bit operands with fp32 sums. fp32
-// values go through it as two fp16 parts, x = hi + lo, each tensor scaled by the
-// power of two that brings its largest magnitude near 2^15: hi has 11 bits, lo
-// the next 11 and its sign one more, so a value keeps 24 bits as long as it is
-// above 2^-17 of the largest, and an absolute 2^-40 of the largest below that.
-// Three part products are summed, small ones first; the fourth, lo lo, is below
-// 2^-24 of the whole, as is a rounding in fp32. (Three bf16 parts need no scale,
-// but six products for the same error: twice the time.)
+// values go through it as three bf16 parts, x = hi + mid + lo exactly: bf16 has
+// fp32's exponents, so every value keeps its 24 bits whatever stands beside it. Six
+// of the nine part products are summed, small ones first; the other three are
+// together below 2^-23 of a product. (Two fp16 parts and three products take half the
+// time, 1024 x 50257 x 768 with gradients 1.12 ms in place of 1.90, but fp16 has 40
+// bits between its largest value and its smallest step: what is further below the
+// largest of whatever shares a scale is lost, and probabilities are.)
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -49,9 +49,6 @@ struct Head {
   int splits;       // runs that dhidden's sum over a piece of the vocabulary is cut into
   float scale;      // what g is held at
   float inv_scale;
-  // fp32: the bits of the largest finite magnitude in the live rows of hidden, and in
-  // the weight. (Non-negative floats order as their bits do, infinity and NaN above all.)
-  uint32_t top_h, top_w;
 };
 
 // The power of two that brings the finite `top` to [2^14, 2^15), within 2^+-100, and
@@ -60,9 +57,6 @@ __device__ __forceinline__ int scale_exponent(float top) {
   if (top == 0.0f) return 0;
   const int e = 14 - ilogbf(top);
   return e < -100 ? -100 : e > 100 ? 100 : e;
-}
-__device__ __forceinline__ int scale_exponent(uint32_t bits) {
-  return scale_exponent(__builtin_bit_cast(float, bits));
 }
 
 // Per live row, for the logits' gradient
@@ -78,10 +72,10 @@ struct RowParam {
 static_assert(sizeof(RowParam) == 32, "the plan counts 32 bytes a row");
 
 // The part products of fp32 operands: (left part, right part), small ones first.
-constexpr int kParts = 2;
-constexpr int kSegs = 3;
-__device__ __forceinline__ int seg_a(int seg) { return seg == 0 ? 1 : 0; }
-__device__ __forceinline__ int seg_b(int seg) { return seg == 1 ? 1 : 0; }
+constexpr int kParts = 3;
+constexpr int kSegs = 6;
+__device__ __forceinline__ int seg_a(int seg) { return 0x001021 >> 4 * seg & 3; }  // 1 2 0 1 0 0
+__device__ __forceinline__ int seg_b(int seg) { return 0x010201 >> 4 * seg & 3; }  // 1 0 2 0 1 0
 
 // ---- Values ---------------------------------------------------------------
 __device__ __forceinline__ u16 bf16_bits(float x) { return __builtin_bit_cast(u16, (__bf16)x); }
@@ -93,12 +87,16 @@ __device__ __forceinline__ float f16_float(u16 b) {
   return (float)__builtin_bit_cast(_Float16, b);
 }
 
-// x = p[0] + p[1] in fp16 parts. An infinity or NaN is its first part alone (the
-// remainder would be NaN).
-__device__ __forceinline__ void split2(float x, u16 p[kParts]) {
-  p[0] = f16_bits(x);
-  const float hi = f16_float(p[0]);
-  p[1] = f16_bits(__builtin_isfinite(hi) ? x - hi : 0.0f);
+// x = p[0] + p[1] + p[2] in bf16 parts: 8 bits each, and the remainders' signs. An
+// infinity or NaN is its first part alone (the remainder would be NaN); a finite value
+// that would round to infinity has bf16's largest.
+__device__ __forceinline__ void split3(float x, u16 p[kParts]) {
+  p[0] = bf16_bits(x);
+  const bool finite = __builtin_isfinite(x);
+  p[0] -= finite && (p[0] & 0x7fff) == 0x7f80;
+  const float r = finite ? x - bf16_float(p[0]) : 0.0f;
+  p[1] = bf16_bits(r);
+  p[2] = bf16_bits(r - bf16_float(p[1]));
 }
 
 template <int DT>
@@ -164,7 +162,7 @@ constexpr float kHugeBase = 0x1p20f;
 
 template <int DT>
 __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
-  if constexpr (DT != kBF16)
+  if constexpr (DT == kF16)
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
                                                   __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
   else
@@ -352,73 +350,16 @@ __global__ void __launch_bounds__(1024) scan_kernel(Call c) {
     head->live = base;
     head->splits = splits;
     set_scale(c, reach, &head->scale, &head->inv_scale);
-    head->top_h = head->top_w = 0;
   }
 }
 
 // ---- Packing --------------------------------------------------------------
-// fp32: the largest finite magnitudes of the weight and, in the last kTopHidden
-// blocks, of the live rows of hidden: what is not finite stays so under any scale,
-// and must not choose one for the rows beside it. The largest of largest in any
-// order is the same number, so the atomics leave nothing to chance; there is one a
-// block of sixteen waves, since they all wait for each other (for 154 MB, one a wave
-// took 165 us, one every four waves 38 us, this 31 us). A wave reads kTopRows rows at
-// once, to have their loads in flight together.
-constexpr int kTopHidden = 16, kTopBlocks = 512, kTopRows = 4;
-__device__ __forceinline__ uint32_t finite_size(uint32_t bits) {
-  bits &= 0x7fffffffu;
-  return bits < 0x7f800000u ? bits : 0;
-}
-__global__ void __launch_bounds__(1024) top_kernel(Call c) {
-  const Plan& p = c.plan;
-  Head* head = reinterpret_cast<Head*>(c.ws + p.o_head);
-  const int first_h = (int)gridDim.x - kTopHidden;
-  const bool is_h = (int)blockIdx.x >= first_h;
-  const int64_t rows = is_h ? head->live : p.vocab, pitch = is_h ? c.hidden_stride : c.weight_stride;
-  const int wave = threadIdx.x / 64, lane = threadIdx.x % 64;
-  const int64_t first = ((int)blockIdx.x - (is_h ? first_h : 0)) * 16 + wave;
-  const int64_t step = (is_h ? kTopHidden : first_h) * 16;
-  uint32_t top = 0;
-  for (int64_t r = first; r < rows; r += kTopRows * step) {
-    const uint32_t* x[kTopRows];  // beyond the last row: the last once more
-#pragma unroll
-    for (int j = 0; j < kTopRows; ++j) {
-      const int64_t at = min(r + j * step, rows - 1);
-      const int64_t row = is_h ? reinterpret_cast<const int*>(c.ws + p.o_rowmap)[at] : at;
-      x[j] = static_cast<const uint32_t*>(is_h ? c.hidden : c.weight) + row * pitch;
-    }
-    const int bulk = (int)p.dim / 4 * 4;
-    for (int k = lane * 4; k < bulk; k += 256) {
-      u32x4 v[kTopRows];
-#pragma unroll
-      for (int j = 0; j < kTopRows; ++j) __builtin_memcpy(&v[j], x[j] + k, 16);
-#pragma unroll
-      for (int j = 0; j < kTopRows; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) top = max(top, finite_size(v[j][i]));
-    }
-    for (int k = bulk + lane; k < p.dim; k += 64)
-#pragma unroll
-      for (int j = 0; j < kTopRows; ++j) top = max(top, finite_size(x[j][k]));
-  }
-#pragma unroll
-  for (int d = 32; d; d >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
-  __shared__ uint32_t tops[16];
-  if (lane == 0) tops[wave] = top;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-#pragma unroll
-    for (int i = 1; i < 16; ++i) top = max(top, tops[i]);
-    if (top != 0) atomicMax(is_h ? &head->top_h : &head->top_w, top);
-  }
-}
-
 // Eight elements from column k of a row, zero beyond `dim`, as 16-bit parts. Rows may
 // start at any element: the memory takes 16-byte loads at any address (loads element
 // by element where rows are not aligned to 16 bytes: 64 x 50000 x 1001 in fp32 with
 // gradients 579 us in place of 511, 8 x 50000 x 1001 in bf16 233 in place of 206).
 template <int DT>
-__device__ __forceinline__ void pack8(const void* src, int64_t at, int k, int dim, float scale,
+__device__ __forceinline__ void pack8(const void* src, int64_t at, int k, int dim,
                                       u32x4 out[kParts]) {
   if constexpr (DT != kF32) {
     if (k + 8 <= dim) {
@@ -442,7 +383,7 @@ __device__ __forceinline__ void pack8(const void* src, int64_t at, int k, int di
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       u16 p[kParts];
-      split2(v[i] * scale, p);
+      split3(v[i], p);
 #pragma unroll
       for (int s = 0; s < kParts; ++s) parts[s][i] = p[s];
     }
@@ -462,7 +403,6 @@ __global__ void __launch_bounds__(256) pack_hidden_kernel(Call c) {
   if (r >= round_up_int(live, (int)kRowPad)) return;
   u16* dst = reinterpret_cast<u16*>(c.ws + p.o_h) + (int64_t)r * p.dimp;
   const bool real = r < live;
-  const float scale = DT == kF32 ? ldexpf(1.0f, scale_exponent(head->top_h)) : 1.0f;
   const int64_t t = real ? reinterpret_cast<const int*>(c.ws + p.o_rowmap)[r] : 0;
   const int64_t at = t * c.hidden_stride;
   if (p.grad && threadIdx.x == 0) {
@@ -473,7 +413,7 @@ __global__ void __launch_bounds__(256) pack_hidden_kernel(Call c) {
   }
   for (int k = threadIdx.x * 8; k < p.dimp; k += 256 * 8) {
     u32x4 v[kParts] = {};
-    if (real) pack8<DT>(c.hidden, at, k, (int)p.dim, scale, v);
+    if (real) pack8<DT>(c.hidden, at, k, (int)p.dim, v);
     for (int s = 0; s < (DT == kF32 ? kParts : 1); ++s)
       *reinterpret_cast<u32x4*>(dst + s * p.rows * p.dimp + k) = v[s];
   }
@@ -516,7 +456,7 @@ __global__ void __launch_bounds__(256) few_rows_kernel(Call c) {
       if (lane == 0) {
         float inv_scale;
         set_scale(c, r, &scale, &inv_scale);
-        *head = {live, splits, scale, inv_scale, 0, 0};
+        *head = {live, splits, scale, inv_scale};
       }
     }
   }
@@ -530,7 +470,7 @@ __global__ void __launch_bounds__(256) few_rows_kernel(Call c) {
   const int r = blockIdx.x, k = ((int)blockIdx.y * 256 + tid) * 8;
   if (k >= p.dimp) return;
   u32x4 v[kParts] = {};
-  if (r < live) pack8<DT>(c.hidden, rowmap[r] * c.hidden_stride, k, (int)p.dim, 1.0f, v);
+  if (r < live) pack8<DT>(c.hidden, rowmap[r] * c.hidden_stride, k, (int)p.dim, v);
   *reinterpret_cast<u32x4*>(reinterpret_cast<u16*>(c.ws + p.o_h) + (int64_t)r * p.dimp + k) = v[0];
 }
 
@@ -541,39 +481,12 @@ __global__ void __launch_bounds__(256) pack_weight_kernel(Call c, int64_t v0) {
   const int64_t r = blockIdx.x;
   u16* dst = reinterpret_cast<u16*>(c.ws + p.o_w) + r * p.dimp;
   const bool real = v0 + r < p.vocab;
-  const float scale =
-      DT == kF32
-          ? ldexpf(1.0f, scale_exponent(reinterpret_cast<const Head*>(c.ws + p.o_head)->top_w))
-          : 1.0f;
   for (int k = threadIdx.x * 8; k < p.dimp; k += 256 * 8) {
     u32x4 v[kParts] = {};
-    if (real) pack8<DT>(c.weight, (v0 + r) * c.weight_stride, k, (int)p.dim, scale, v);
+    if (real) pack8<DT>(c.weight, (v0 + r) * c.weight_stride, k, (int)p.dim, v);
     for (int s = 0; s < (DT == kF32 ? kParts : 1); ++s)
       *reinterpret_cast<u32x4*>(dst + s * p.piece * p.dimp + k) = v[s];
   }
-}
-
-// What a sum over scaled operands is multiplied by to undo their scales: one
-// factor each, since the two together may leave fp32's range.
-template <int DT>
-__device__ __forceinline__ float undo_h(const Head* head) {
-  return DT == kF32 ? ldexpf(1.0f, -scale_exponent(head->top_h)) : 1.0f;
-}
-template <int DT>
-__device__ __forceinline__ float undo_w(const Head* head) {
-  return DT == kF32 ? ldexpf(1.0f, -scale_exponent(head->top_w)) : 1.0f;
-}
-// A logit from its sum. The factors are powers of two.
-template <int DT>
-__device__ __forceinline__ float logit_of(float sum, const Head* head) {
-  return DT == kF32 ? sum * undo_h<DT>(head) * undo_w<DT>(head) : sum;
-}
-// What a logit's sum is multiplied by to be an exponent of two. (Where the scales
-// of both operands go out of fp32's range together, so do the logits: all zero.)
-template <int DT>
-__device__ __forceinline__ float exponent_factor(const Head* head, float inv_temp) {
-  const float f = inv_temp * kLog2e;
-  return DT == kF32 ? ldexpf(f, -scale_exponent(head->top_h) - scale_exponent(head->top_w)) : f;
 }
 
 // ---- The product ----------------------------------------------------------
@@ -952,9 +865,7 @@ __device__ __forceinline__ void Gather<DT>::wave(int64_t id) const {
   // lane l holds rows l / 16 * 4 + 0..3 of column l % 16
   if (mine && q / 4 == lane / 16) {
     const float sum = q % 4 == 0 ? acc[0] : q % 4 == 1 ? acc[1] : q % 4 == 2 ? acc[2] : acc[3];
-    const Head* head = reinterpret_cast<const Head*>(c.ws + p.o_head);
-    const float z = logit_of<DT>(sum, head);
-    (c.k == 0 ? reinterpret_cast<float*>(c.ws + p.o_entry) : c.logit)[t * K + k] = z;
+    (c.k == 0 ? reinterpret_cast<float*>(c.ws + p.o_entry) : c.logit)[t * K + k] = sum;
   }
 }
 
@@ -973,7 +884,7 @@ __global__ void __launch_bounds__(256) gather_kernel(Gather<DT> g) {
 // Forward: the tile's rows m are vocabulary, its columns n live rows. Each wave
 // leaves, of its stretch of the vocabulary, a base near its largest logit (as an
 // exponent of two), the sum of the exponentials relative to it, and the sum of
-// the logits' sums.
+// the logits.
 // Sixteen columns of 128 results, four 16-bit values in a register pair (`part`,
 // one for each square), become rows of 256 bytes through 4 KB of LDS that are the
 // wave's own once the stages are done with: then a store has 16 bytes a lane and four whole rows, in place of 8 bytes
@@ -1001,7 +912,6 @@ __device__ __forceinline__ void turn_rows(lds_char* turn, const u32x2 (&part)[8]
 
 template <int DT>
 struct StatEpi {
-  const Head* head;
   Gather<DT> gather;  // what the launch's first blocks do, where it has any for that
   float2* stat;
   float* sum;       // nullptr where nobody asks for it
@@ -1018,7 +928,7 @@ struct StatEpi {
     const int lane = threadIdx.x % 64;
     const int m_hi = vocab - m_base;
     if (m0 >= round_up_int(m_hi, (int)kStatRows) || n0 >= n_ext) return;
-    const float f = exponent_factor<DT>(head, inv_temp);
+    const float f = inv_temp * kLog2e;
     const bool edge = m0 + (int)kStatRows > m_hi;  // some of it is beyond the vocabulary
     // These exponentials are the kernel's second cost after the products: a maximum,
     // one fused multiply-add, the power of two (four times an addition's time) and
@@ -1085,7 +995,6 @@ struct StatEpi {
 // know either.
 template <int DT>
 struct GradEpi {
-  const Head* head;
   const RowParam* rows;
   u16* g;
   int64_t plane, ld;
@@ -1099,7 +1008,7 @@ struct GradEpi {
                                        lds_char* turn) {
     constexpr int kPlanes = DT == kF32 ? kParts : 1;
     const int lane = threadIdx.x % 64;
-    const float f = exponent_factor<DT>(head, inv_temp);
+    const float f = inv_temp * kLog2e;
     const bool edge = m0 + MI * 16 > m_ext || n0 + NJ * 16 > n_ext;
     RowParam rps[NJ];  // all loads on their way before the first is waited for
 #pragma unroll
@@ -1152,7 +1061,7 @@ struct GradEpi {
           const float x = acc[i][j][r];
           if constexpr (DT == kF32) {
             u16 p[kParts];
-            split2(x, p);
+            split3(x, p);
             for (int s = 0; s < kParts; ++s) parts[s][r] = p[s];
           } else {
             parts[0][r] = DT == kBF16 ? bf16_bits(x) : f16_bits(x);
@@ -1224,7 +1133,7 @@ struct WeightEpi {
   __device__ __forceinline__ void tile(int m0, int n0, int n_ext, int, f32x4 (&acc)[MI][NJ],
                                        lds_char* turn) {
     const int lane = threadIdx.x % 64;
-    const float s = head->inv_scale, uh = undo_h<DT>(head);
+    const float s = head->inv_scale;
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
       if constexpr (DT != kF32) {
@@ -1232,7 +1141,7 @@ struct WeightEpi {
           u32x2 packed[MI];
 #pragma unroll
           for (int i = 0; i < MI; ++i) {
-            const f32x4 x = acc[i][j] * uh * s;
+            const f32x4 x = acc[i][j] * s;
             u16 b[4];
 #pragma unroll
             for (int r = 0; r < 4; ++r) b[r] = DT == kBF16 ? bf16_bits(x[r]) : f16_bits(x[r]);
@@ -1258,7 +1167,7 @@ struct WeightEpi {
 #pragma unroll
       for (int i = 0; i < MI; ++i) {
         const int m = m0 + i * 16 + lane / 16 * 4;
-        const f32x4 x = acc[i][j] * uh * s;
+        const f32x4 x = acc[i][j] * s;
         if (m + 4 <= m_ext) {
           store4<DT>(out, (v0 + n) * ld + m, x, wide >= 4);
         } else {
@@ -1326,7 +1235,6 @@ __global__ void __launch_bounds__(256) loss_kernel(Call c) {
   // base and sum s of 2^(z f - base) over the vocabulary, f = log2(e) / temperature
   const float2* stat = reinterpret_cast<const float2*>(c.ws + p.o_stat) + at * p.stat_cols;
   const int cols = (int)((p.vocab + kStatRows - 1) / kStatRows);
-  const Head* head = reinterpret_cast<const Head*>(c.ws + p.o_head);
   float m = -INFINITY;
   for (int i = tid; i < cols; i += 256)
     if (stat[i].y > 0.0f) m = fmaxf(m, stat[i].x);
@@ -1348,17 +1256,12 @@ __global__ void __launch_bounds__(256) loss_kernel(Call c) {
   const float log2s = log2f(s), lse = (float)(((double)m + log2s) * 0.6931471805599453);
   // base - z f in one rounding: added to log2 s it is the loss in powers of two, and
   // exact where the target is the largest logit, since the sum has the same term.
-  // (fp32's factor f of the sums is this one times a power of two.)
   const auto behind = [m, f](float z) { return fmaf(-z, f, m); };
   if (c.k == 0) {
     if (tid == 0) {
       const float zy = zs[0];
       float loss = (behind(zy) + log2s) * kLn2;
-      if (c.smoothing != 0.0f) {
-        const bool f32 = p.dtype == kF32;
-        plain = f32 ? logit_of<kF32>(plain, head) : plain;
-        loss += c.smoothing * (zy - plain / (float)p.vocab);
-      }
+      if (c.smoothing != 0.0f) loss += c.smoothing * (zy - plain / (float)p.vocab);
       if (c.z_loss != 0.0f) loss += c.z_loss * lse * lse;
       c.loss[t] = loss;
       c.lse[t] = lse;
@@ -1442,7 +1345,7 @@ __global__ void __launch_bounds__(64) entry_kernel(Call c, int64_t v0) {
     const float x = rp.a * (exp_f(below > 0.0f ? 0.0f : below) - same / total);
     if constexpr (DT == kF32) {
       u16 parts[kParts];
-      split2(x, parts);
+      split3(x, parts);
       for (int s = 0; s < kParts; ++s) g[s * p.rows * p.piece + m] = parts[s];
     } else {
       g[m] = DT == kBF16 ? bf16_bits(x) : f16_bits(x);
@@ -1474,7 +1377,7 @@ __global__ void __launch_bounds__(64) dhidden_kernel(Call c, bool wide) {
       for (int i = 0; i < 8; ++i)
         if (q + i < splits) x += v[i];
     }
-    x = x * undo_w<DT>(head) * head->inv_scale;
+    x = x * head->inv_scale;
   }
   if (k + 4 <= p.dim) {
     store4<DT>(c.dhidden, t * c.dhidden_stride + k, x, wide);
@@ -1522,11 +1425,6 @@ void rows_and_hidden(const Call& c, hipStream_t st) {
     classify_kernel<<<(unsigned)((p.tokens + 3) / 4), 256, 0, st>>>(
         c, reinterpret_cast<uint8_t*>(c.ws + p.o_state));
   scan_kernel<<<1, 1024, 0, st>>>(c);
-  if (DT == kF32) {
-    const int64_t w_blocks = (p.vocab + 16 * kTopRows - 1) / (16 * kTopRows);
-    const int blocks = (int)(w_blocks < kTopBlocks ? w_blocks : kTopBlocks) + kTopHidden;
-    top_kernel<<<blocks, 1024, 0, st>>>(c);
-  }
   if (p.tokens > 0)
     pack_hidden_kernel<DT><<<(unsigned)p.rows, 256, 0, st>>>(c);
 }
@@ -1569,8 +1467,7 @@ void loss_type(const Call& c, hipStream_t st) {
     const u16* w = piece_weight<DT>(c, v0, &ldw, st);
     const int64_t real = p.vocab - v0 < p.piece ? p.vocab - v0 : p.piece;
     const Gather<DT> gather{c, w, ldw, v0, (int)real};
-    StatEpi<DT> epi{reinterpret_cast<const Head*>(c.ws + p.o_head), gather,
-                    reinterpret_cast<float2*>(c.ws + p.o_stat),
+    StatEpi<DT> epi{gather, reinterpret_cast<float2*>(c.ws + p.o_stat),
                     c.smoothing != 0.0f ? reinterpret_cast<float*>(c.ws + p.o_sum) : nullptr,
                     p.stat_cols, 1.0f / c.temperature, (int)v0, (int)p.vocab};
     Product g = logits_product<DT>(c, w, ldw, real);
@@ -1598,7 +1495,7 @@ void grad_type(const Call& c, hipStream_t st) {
     const int64_t real = p.vocab - v0 < p.piece ? p.vocab - v0 : p.piece;
     // g of the piece
     Product g = logits_product<DT>(c, w, ldw, real);
-    GradEpi<DT> ge{head, reinterpret_cast<const RowParam*>(c.ws + p.o_rowp), gbuf, p.rows * p.piece,
+    GradEpi<DT> ge{reinterpret_cast<const RowParam*>(c.ws + p.o_rowp), gbuf, p.rows * p.piece,
                    p.piece, 1.0f / c.temperature, (int)v0, (int)real, c.smoothing != 0.0f};
     logits<DT>(p, g, ge, st);
     if (c.k > 0 && p.tokens > 0) entry_kernel<DT><<<(unsigned)p.tokens, 64, 0, st>>>(c, v0);

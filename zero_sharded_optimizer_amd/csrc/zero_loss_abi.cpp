@@ -132,7 +132,7 @@ void choose_tile(zloss::Plan* p) {
                                     {256, 64, 512, {0.85, 1.15, 1.15}, 3},
                                     {128, 64, 768, {0.70, 0.92, 1.05}, 3}};
   const int64_t rows = std::min(p->piece, p->vocab);
-  const double steps = (double)(p->dimp / 64) * (p->planes > 1 ? 3 : 1);
+  const double steps = (double)(p->dimp / 64) * (p->planes > 1 ? 6 : 1);
   double best = HUGE_VAL;
   for (const Kind& k : kinds) {
     if (k.n == 256 && p->tokens <= zloss::kFewTokens) continue;
@@ -156,7 +156,7 @@ zloss::Plan make_plan(const zero_head& h, bool grad) {
   p.vocab = h.vocab;
   p.dim = h.dim;
   p.dtype = h.dtype;
-  p.planes = h.dtype == ZERO_LOSS_F32 ? 2 : 1;
+  p.planes = h.dtype == ZERO_LOSS_F32 ? 3 : 1;
   p.grad = grad;
   p.rows = round_up(std::max<int64_t>(h.tokens, 1), zloss::kRowPad);
   p.dimp = round_up(h.dim, zloss::kDimPad);

@@ -23,7 +23,7 @@ constexpr int kFewTokens = 64;
 struct Plan {
   int64_t tokens, vocab, dim;
   int dtype;
-  int planes;        // 16-bit parts per value: 2 for fp32, else 1
+  int planes;        // 16-bit parts per value: 3 for fp32, else 1
   bool grad;
   bool pack_w;       // the weight goes through an aligned, padded copy, piece by piece
   int64_t rows;      // tokens padded to kRowPad
@@ -33,7 +33,7 @@ struct Plan {
   int64_t stat_cols; // softmax partials per token
   int acc_tiles;     // tiles that the slabs of dhidden's sum have room for
   // workspace offsets, bytes
-  size_t o_head;     // Head: live count, scale
+  size_t o_head;     // Head: live count, runs, scale
   size_t o_rowmap;   // int32[rows]: live position -> token
   size_t o_pos;      // int32[tokens]: token -> live position, -1 empty, -2 bad
   size_t o_state;    // uint8[tokens]: distillation's row states
