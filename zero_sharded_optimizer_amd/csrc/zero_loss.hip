@@ -51,11 +51,11 @@ struct Head {
   float inv_scale;
 };
 
-// The power of two that brings the finite `top` to [2^14, 2^15), within 2^+-100, and
-// 1 for zero.
-__device__ __forceinline__ int scale_exponent(float top) {
+// The power of two that brings the finite `top` to [2^to, 2^(to + 1)), within 2^+-100,
+// and 1 for zero.
+__device__ __forceinline__ int scale_exponent(float top, int to) {
   if (top == 0.0f) return 0;
-  const int e = 14 - ilogbf(top);
+  const int e = to - ilogbf(top);
   return e < -100 ? -100 : e > 100 ? 100 : e;
 }
 
@@ -228,14 +228,15 @@ __device__ __forceinline__ Reach row_reach(const Call& c, int64_t t) {
   return top < INFINITY ? Reach{top, u} : Reach{0.0f, 0.0f};
 }
 
-// The scale that g is held at. The largest |g| a row can have comes to (2^13,
-// 2^15], inside fp16's range with 27 bits below it that are not subnormal; and of
+// The scale that g is held at. In fp16 the largest |g| a row can have comes to (2^13,
+// 2^15], inside its range with 27 bits below it that are not subnormal; in bf16 (and
+// fp32's parts) to (1/2, 2], so that no product overflows whose result does not; and of
 // the factors that do so, the one that makes the largest row's pull on its target
 // a power of two: with one upstream gradient for all rows, as a mean has, the -1
 // of every row the model is unsure of is then exact, in place of all of them being
 // rounded the same way.
 __device__ __forceinline__ void set_scale(const Call& c, Reach r, float* scale, float* inv_scale) {
-  const int e = scale_exponent(r.top);
+  const int e = scale_exponent(r.top, c.plan.dtype == kF16 ? 14 : 0);
   // pull (1 - smoothing) = part 2^q: dividing by the part, in [1, 2), leaves 2^q
   const float pull = r.pull * (1.0f - c.smoothing);
   const float part = pull > 0x1p-80f && pull < 0x1p80f ? scalbnf(pull, -ilogbf(pull)) : 1.0f;
