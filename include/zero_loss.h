@@ -98,7 +98,8 @@ typedef struct {
   int32_t index_dtype;    /* a zero_index_dtype */
   int32_t logit_dtype;    /* a zero_loss_dtype */
   int32_t reserved;       /* must be 0 */
-  double temperature;     /* finite, > 0 */
+  double temperature;     /* > 0, its square neither infinite nor subnormal as floats:
+                             1.1e-19 to 1.8e19 */
 } zero_distill_params;
 
 /* Gradients: device buffers the caller owns; rows contiguous, strides in

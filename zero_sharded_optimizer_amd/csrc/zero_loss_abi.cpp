@@ -292,9 +292,12 @@ zero_status check_distill(const zero_head& h, const zero_distill_params* p) {
   if (!aligned(p->index, (uintptr_t)index_size(p->index_dtype)) ||
       !aligned(p->logit, (uintptr_t)dtype_size(p->logit_dtype)))
     return fail(ZERO_EINVAL, "index and logit must be aligned to their element size");
-  if (!(std::isfinite(p->temperature) && p->temperature > 0.0 &&
-        std::isfinite(1.0f / (float)p->temperature) && (float)p->temperature > 0.0f))
-    return fail(ZERO_EINVAL, "temperature must be finite and > 0");
+  // What the kernels form of it, as floats: its square, and log2(e) over it, which lies
+  // further from either end of the range.
+  const float t = (float)p->temperature;
+  if (!(t > 0.0f && std::isnormal(t * t)))
+    return fail(ZERO_EINVAL, "temperature must be > 0, its square (as floats) neither infinite "
+                             "nor subnormal");
   return ZERO_OK;
 }
 
