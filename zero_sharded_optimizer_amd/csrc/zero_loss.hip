@@ -576,14 +576,15 @@ __device__ __forceinline__ uint32_t copy_offset(const Operand& o, int r0, int in
 // 16 bytes a lane from base + offset to LDS, lane after lane from `to` (both the
 // same in the whole wave). The compiler does not see it as a load, and so does
 // not hold up the transposing reads, which it cannot tell apart from the stage
-// that is being written, until it has landed: the waits are written out below.
+// that is being written, until it has landed: the waits are written out below. It
+// sets M0 itself (and may do so in the addition that forms `to`); the load needs an
+// instruction's time after that.
 __device__ __forceinline__ void copy_to_lds(const char* base, uint32_t offset, uint32_t to) {
   asm volatile(
-      "s_mov_b32 m0, %0\n\t"
       "s_nop 0\n\t"
       "global_load_lds_dwordx4 %1, %2"
       :
-      : "s"(to), "v"(offset), "s"(base)
+      : "{m0}"(to), "v"(offset), "s"(base)
       : "memory");
 }
 
