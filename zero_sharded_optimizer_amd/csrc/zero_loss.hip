@@ -207,6 +207,13 @@ __device__ __forceinline__ int state_of(int seen) {
   return seen & 2 ? kBad : seen & 1 ? kLive : kEmpty;
 }
 
+// The teacher's logit of entry k of row t; padding has -inf.
+__device__ __forceinline__ float entry_logit(const Call& c, int64_t t, int k) {
+  return load_index(c.target, t * c.index_stride + k, c.index64) < 0
+             ? -INFINITY
+             : load_any(c.teacher, t * c.logit_stride + k, c.teacher_dtype);
+}
+
 // Distillation: one wave a row.
 __global__ void __launch_bounds__(256) classify_kernel(Call c, uint8_t* state) {
   const int64_t t = (int64_t)blockIdx.x * 4 + threadIdx.x / 64;
@@ -1272,12 +1279,10 @@ __global__ void __launch_bounds__(256) loss_kernel(Call c) {
   }
   float top = -INFINITY;
   for (int k = tid; k < K; k += 256) {
-    const int64_t i = load_index(c.target, t * c.index_stride + k, c.index64);
-    const float l = i < 0 ? -INFINITY
-                          : load_any(c.teacher, t * c.logit_stride + k, c.teacher_dtype) * inv_temp;
-    if (i < 0) c.logit[t * K + k] = 0.0f;
-    ls[k] = l;
-    top = fmaxf(top, l);
+    const float l = entry_logit(c, t, k);
+    if (l == -INFINITY) c.logit[t * K + k] = 0.0f;
+    ls[k] = l * inv_temp;
+    top = fmaxf(top, ls[k]);
   }
   top = block_max<4>(top, red);
   float total = 0.0f;
@@ -1317,12 +1322,10 @@ __global__ void __launch_bounds__(64) entry_kernel(Call c, int64_t v0) {
   const float inv_temp = 1.0f / c.temperature;
   float top = -INFINITY;
   for (int k = lane; k < c.k; k += 64) {
-    const int64_t i = load_index(c.target, t * c.index_stride + k, c.index64);
-    const float l = i < 0 ? -INFINITY
-                          : load_any(c.teacher, t * c.logit_stride + k, c.teacher_dtype) * inv_temp;
-    idx[k] = i < 0 ? -1 : (int)i;
-    pk[k] = l;
-    top = fmaxf(top, l);
+    const float l = entry_logit(c, t, k);
+    idx[k] = l == -INFINITY ? -1 : (int)load_index(c.target, t * c.index_stride + k, c.index64);
+    pk[k] = l * inv_temp;
+    top = fmaxf(top, pk[k]);
   }
   top = wave_max(top);
   float total = 0.0f;
