@@ -200,14 +200,18 @@ def _handle(stream, like):
     return _stream_handle(stream, like)
 
 
+def _check_workspace(workspace):
+    import torch
+    if workspace is not None and (not isinstance(workspace, torch.Tensor) or not workspace.is_cuda
+                                  or not workspace.is_contiguous()):
+        raise ValueError("workspace: must be a contiguous GPU tensor")
+
+
 def _workspace(head, want_grad, workspace, like):
     import torch
     need = _workspace_bytes(head, want_grad)
     if workspace is None:
         return torch.empty(need, dtype=torch.uint8, device=like.device), need
-    if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda \
-            or not workspace.is_contiguous():
-        raise ValueError("workspace: must be a contiguous GPU tensor")
     return workspace, workspace.numel() * workspace.element_size()
 
 
@@ -217,6 +221,7 @@ def linear_xent(hidden, weight, target, ignore_index: int = -100, label_smoothin
     import torch
     head = _head(hidden, weight)
     params = _xent_params(hidden, target, ignore_index, label_smoothing, z_loss)
+    _check_workspace(workspace)
     _one_device(stream, hidden, weight, target, workspace)
     lib = _abi.load()
     with _on_stream(stream, hidden):
@@ -238,6 +243,7 @@ def linear_distill(hidden, weight, index, logit, temperature: float = 1.0, works
     import torch
     head = _head(hidden, weight)
     params = _distill_params(hidden, index, logit, temperature)
+    _check_workspace(workspace)
     _one_device(stream, hidden, weight, index, logit, workspace)
     lib = _abi.load()
     with _on_stream(stream, hidden):
@@ -288,6 +294,7 @@ def _grad(entry, hidden, weight, head, params, saved, extra, upstream, dhidden, 
     if dweight is not None:
         _matrix(dweight, "dweight", weight.dtype, weight.shape)
     _check_saved(saved.lse, "saved.lse", (hidden.shape[0],))
+    _check_workspace(workspace)
     _one_device(stream, hidden, weight, *tensors, saved.lse, dhidden, dweight, workspace,
                 upstream if isinstance(upstream, torch.Tensor) else None)
     with _on_stream(stream, hidden):
