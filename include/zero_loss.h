@@ -31,14 +31,16 @@
  * units; softmax statistics, losses and the sum over the vocabulary of dhidden
  * in fp32. loss and lse are rounded by the size of the row's largest logit over the
  * temperature, and so is what a probability in the gradient is formed from (beyond
- * some 2^20 that is more than the difference of neighbours). g is rounded once to the given type for its products (bf16; fp16
- * after a scaling that keeps the largest |u_t| near 2^14, undone in fp32 before
- * the result is rounded). In fp32 hidden, weight and g are each held as three bf16
- * parts, all 24 bits of every value, and six of the nine part products are summed:
- * what is left out is below 2^-23 of each product. A row with an infinity or a NaN
- * leaves the other rows' losses and dhidden as they are; in fp32 a product with an
- * infinity may be NaN where it would otherwise be infinite. The same call gives the
- * same bits: nothing is summed in an order left to chance.
+ * some 2^20 that is more than the difference of neighbours). g is rounded once to
+ * the given type for its products: in bf16 under a scale that keeps the largest
+ * |u_t| near 1, in fp16 under one that keeps it near 2^14 (what is below 2^-28 of it
+ * then has fewer bits, and none below 2^-38), undone in fp32 before the result is
+ * rounded. In fp32 hidden, weight and g are each held as three bf16 parts, all 24
+ * bits of every value, and six of the nine part products are summed: what is left
+ * out is below 2^-23 of each product. A row with an infinity or a NaN leaves the
+ * other rows' losses and dhidden as they are; in fp32 a product with an infinity may
+ * be NaN where it would otherwise be infinite. The same call gives the same bits:
+ * nothing is summed in an order left to chance.
  *
  * Conventions are those of zero_adam.h: caller-owned device buffers, work
  * enqueued on `stream`, arguments validated before any HIP call, status codes,

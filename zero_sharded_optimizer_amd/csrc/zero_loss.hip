@@ -122,10 +122,10 @@ __device__ __forceinline__ void store_value(void* p, int64_t i, float x) {
 }
 
 // Four values of a result to four consecutive elements; `wide`: the address suits
-// one store (wide stores at any address: 64 x 50000 x 1001 in fp32 with gradients 600
-// us in place of 508). Results, and g, are stored past the caches' own choice of what to keep
-// (non-temporal): they are larger than the caches, and what they would push out, the
-// weights and hidden states, is still wanted (40 tokens x 131072 x 2048 with
+// one store (one store at any address is no faster: 64 x 50000 x 1001 in fp32 with
+// gradients 620 us either way). Results, and g, are stored past the caches' own choice of
+// what to keep (non-temporal): they are larger than the caches, and what they would push
+// out, the weights and hidden states, is still wanted (40 tokens x 131072 x 2048 with
 // gradients: 428 us in place of 487; 1000 x 32000 x 2048 in fp16: 511 in place of 529).
 template <int DT>
 __device__ __forceinline__ void store4(void* p, int64_t i, f32x4 x, bool wide) {
@@ -274,11 +274,12 @@ __device__ __forceinline__ RowParam row_param(const Call& c, int64_t t, float sc
 // dhidden has few tiles, [live, dim], and a long sum, over the piece's vocabulary,
 // which may be cut into runs. A tile takes its run's steps and, with the slab that is
 // written and read again, about sixteen more (taking four made 1600 live rows x
-// 65536 x 2048 4% slower, nothing faster). Few tokens: the number of runs with which the rounds of 512 tiles that the chip holds
-// at once end soonest. Else the tiles are started as dweight's of the same launch
-// end: `full` rounds of 256, and `rest` in one more; they are done at the first time
-// at which the units that were free from the start of that round, and those that
-// were from its end, have had time for them all. Lane l looks at l + 1 runs.
+// 65536 x 2048 4% slower, nothing faster). Few tokens: the number of runs with which the
+// rounds of 512 tiles that the chip holds at once end soonest. Else the tiles are
+// started as dweight's of the same launch end: `full` rounds of 256, and `rest` in one
+// more; they are done at the first time at which the units that were free from the
+// start of that round, and those that were from its end, have had time for them all.
+// Lane l looks at l + 1 runs.
 __device__ __forceinline__ int choose_splits(const Call& c, int live) {
   const Plan& p = c.plan;
   const bool few = p.tokens <= kFewTokens;
@@ -365,7 +366,7 @@ __global__ void __launch_bounds__(1024) scan_kernel(Call c) {
 // Eight elements from column k of a row, zero beyond `dim`, as 16-bit parts. Rows may
 // start at any element: the memory takes 16-byte loads at any address (loads element
 // by element where rows are not aligned to 16 bytes: 64 x 50000 x 1001 in fp32 with
-// gradients 579 us in place of 511, 8 x 50000 x 1001 in bf16 233 in place of 206).
+// gradients 697 us in place of 620, the loss of 8 x 50000 x 1001 in bf16 79 in place of 65).
 template <int DT>
 __device__ __forceinline__ void pack8(const void* src, int64_t at, int k, int dim,
                                       u32x4 out[kParts]) {
@@ -532,11 +533,12 @@ struct Product {
 // transposing LDS read, four inner steps of 16 rows a time.
 //
 // What bounds it. A 256 x 256 tile's step is 2048 cycles of matrix instructions on
-// each SIMD and takes some 2700: the matrix units are busy 77% of the time at 1.82
-// GHz, which is what the card's power allows at that load (a large library product
-// here has them busy 80% at 1.71 GHz, for 1.08 times the rate). 8192 x 131072 x 4096
-// makes its logits at 1.40 PFLOP/s; at 768 inner steps a tile's start and its
-// epilogue, which nothing overlaps, leave 0.97. Measured against it and slower:
+// each SIMD and takes some 2650: with the logits of 8192 x 131072 x 4096 (6.0 ms, 1.46
+// PFLOP/s) the matrix units are busy 77% of the time at 1.75 GHz, which is what the card's
+// power allows at that load; the library's product of these sizes, without the softmax,
+// has them busy 82% at 1.73 GHz (6.0 ms). At 768 inner dimensions a tile's start and its
+// epilogue, which nothing overlaps, leave 49% at 2.13 GHz, 1.04 PFLOP/s.
+// Measured against it and slower (each beside what it was then):
 // four waves of 128 x 128 with the sums in accumulation registers (a third less LDS
 // reading, but nobody to work while a wave waits; 27.7 ms in place of 26.6 for the
 // whole of that case), a ring of five stages of 32 steps with a meeting each (27.1 in
@@ -563,8 +565,8 @@ __device__ __forceinline__ int first_step(int m, int tile_rows, int steps) {
   return m / tile_rows * 5 % steps;
 }
 
-// Byte offsets, from the tile's corner (r0 < o.rows: a tile starts on a real row), that lane `l` of wave `w` copies from
-// with its i-th instruction of 64 groups.
+// Byte offsets, from the tile's corner (r0 < o.rows: a tile starts on a real row), that
+// a lane copies from with its wave's `instr`-th instruction of 64 groups.
 template <bool T, int R>
 __device__ __forceinline__ uint32_t copy_offset(const Operand& o, int r0, int instr, int lane) {
   if constexpr (!T) {
@@ -576,7 +578,8 @@ __device__ __forceinline__ uint32_t copy_offset(const Operand& o, int r0, int in
     const int k = instr * (64 / kGroups) + lane / kGroups;
     const int turn = (k & 3) | ((k >> 3) & 1) << 2;
     const int group = (lane % kGroups) ^ (turn << 1);
-    return (uint32_t)k * (uint32_t)(o.ld * 2) + (uint32_t)(min(r0 + group * 8, o.rows - 8) - r0) * 2;
+    return (uint32_t)k * (uint32_t)(o.ld * 2) +
+           (uint32_t)(min(r0 + group * 8, o.rows - 8) - r0) * 2;
   }
 }
 
@@ -725,8 +728,9 @@ __device__ __forceinline__ void product_block(const Product& g, Epi epi, int blo
   // Operand q of a half step, in the order the matrix instructions want them.
   const auto read_part = [&](int stage, int ks, int q, u32x4 (&fa)[MI], u32x4 (&fb)[NJ]) INLINE {
     lds_char* ta = lds + stage * S::kStage;
+    const int j = q == 0 ? 0 : q - 1;
     if (q == 1) fa[0] = fragment<TA, BM>(ta, wm, ks, lane);
-    else if (q <= NJ) fb[q == 0 ? 0 : q - 1] = fragment<TB, BN>(ta + S::kStageB, wn + (q == 0 ? 0 : q - 1) * 16, ks, lane);
+    else if (q <= NJ) fb[j] = fragment<TB, BN>(ta + S::kStageB, wn + j * 16, ks, lane);
     else fa[q - NJ] = fragment<TA, BM>(ta, wm + (q - NJ) * 16, ks, lane);
   };
   // Multiplies one half step, row by row of the wave's tile, and between the rows
@@ -890,15 +894,12 @@ __global__ void __launch_bounds__(256) gather_kernel(Gather<DT> g) {
 // A wave holds MI x NJ squares of 16 x 16: column n0 + 16 j + lane % 16, rows
 // m0 + 16 i + lane / 16 * 4 + 0..3.
 
-// Forward: the tile's rows m are vocabulary, its columns n live rows. Each wave
-// leaves, of its stretch of the vocabulary, a base near its largest logit (as an
-// exponent of two), the sum of the exponentials relative to it, and the sum of
-// the logits.
 // Sixteen columns of 128 results, four 16-bit values in a register pair (`part`,
 // one for each square), become rows of 256 bytes through 4 KB of LDS that are the
-// wave's own once the stages are done with: then a store has 16 bytes a lane and four whole rows, in place of 8 bytes
-// and sixteen pieces of 32. put(row, group, value) gets the rows' 16-byte groups.
-// Groups are exchanged by their row, so that neither side meets a bank twice.
+// wave's own once the stages are done with: then a store has 16 bytes a lane and four
+// whole rows, in place of 8 bytes and sixteen pieces of 32. put(row, group, value) gets
+// the rows' 16-byte groups. Groups are exchanged by their row, so that neither side meets
+// a bank twice.
 template <class Put>
 __device__ __forceinline__ void turn_rows(lds_char* turn, const u32x2 (&part)[8], Put put) {
   const int lane = threadIdx.x % 64, r = lane % 16, g = lane / 16;
@@ -919,6 +920,10 @@ __device__ __forceinline__ void turn_rows(lds_char* turn, const u32x2 (&part)[8]
   asm volatile("" ::: "memory");
 }
 
+// Forward: the tile's rows m are vocabulary, its columns n live rows. Each wave
+// leaves, of its stretch of the vocabulary, a base near its largest logit (as an
+// exponent of two), the sum of the exponentials relative to it, and the sum of
+// the logits.
 template <int DT>
 struct StatEpi {
   Gather<DT> gather;  // what the launch's first blocks do, where it has any for that
@@ -941,7 +946,7 @@ struct StatEpi {
     const bool edge = m0 + (int)kStatRows > m_hi;  // some of it is beyond the vocabulary
     // These exponentials are the kernel's second cost after the products: a maximum,
     // one fused multiply-add, the power of two (four times an addition's time) and
-    // the sum are 26 cycles a logit, 3 us a tile that takes 16 for 768 inner steps.
+    // the sum are 26 cycles a logit, 3 us a tile that takes 16 for 768 dimensions.
     // What only some tiles need is kept out of the others' way.
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
@@ -1406,8 +1411,9 @@ template <int DT, bool TA, bool TB, int BM, int BN, int STAGES, class Epi>
 void product_tiles(const Product& g, const Epi& epi, int64_t most_split, hipStream_t st) {
   int64_t total = (int64_t)((g.m + BM - 1) / BM) * ((g.n + BN - 1) / BN);
   if (g.split && total < most_split) total = most_split;
+  const unsigned blocks = (unsigned)((total + 7) / 8 * 8 + g.beside);
   product_kernel<DT, TA, TB, BM, BN, STAGES, Epi>
-      <<<(unsigned)((total + 7) / 8 * 8 + g.beside), Shape<BM, BN, STAGES>::kThreads, 0, st>>>(g, epi);
+      <<<blocks, Shape<BM, BN, STAGES>::kThreads, 0, st>>>(g, epi);
 }
 
 // The logits, in the plan's tiles.

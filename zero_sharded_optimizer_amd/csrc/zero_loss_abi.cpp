@@ -81,13 +81,14 @@ zero_status check_head(const zero_head* h) {
 }
 
 // Vocabulary rows per piece. The largest allowed has 512 MiB of g, or of packed
-// weights (256 MiB, what the chip's last cache holds, is 0.5 to 3% slower for the
-// larger problems: dhidden's sum is then read and written more often; 128 MiB is
-// another 1 to 7%). Smaller ones are taken where the rounds
-// of 256 tiles that the chip holds at once come out fuller, in all: the logits'
-// tiles [piece, tokens] take dim / 64 steps each, dweight's [dim, piece] tokens / 64,
-// either about four steps more, and a piece about eight in launches. (dhidden's
-// tiles fill up dweight's last round.)
+// weights, or 2048 rows where those are more (g: beyond 2^17 tokens, some 43000 in fp32;
+// 4 GiB at 2^20 tokens, 12 GiB in fp32). 256 MiB, what the chip's last cache holds, is
+// 0.5 to 3% slower for the larger problems: dhidden's sum is then read and written more
+// often; 128 MiB is another 1 to 7%. Smaller pieces are taken where the rounds of 256
+// tiles that the chip holds at once come out fuller, in all: the logits' tiles [piece,
+// tokens] take dim / 64 steps each, dweight's [dim, piece] tokens / 64, either about four
+// steps more, and a piece about eight in launches. (dhidden's tiles fill up dweight's
+// last round.)
 int64_t choose_piece(const zloss::Plan& p, int64_t whole) {
   constexpr int64_t kPieceBytes = INT64_C(512) << 20;
   int64_t most = std::min<int64_t>(whole, INT64_C(1) << 21);
