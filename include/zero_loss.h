@@ -89,8 +89,8 @@ typedef struct {
 } zero_xent_params;
 
 /* A teacher's top-K entries. index < 0 is padding, and so is a logit of -inf.
- * An index that stands more than once in a row counts with the sum of its
- * probabilities. */
+ * Of an index that stands more than once in a row every entry has its own term in the
+ * loss, and the gradient has the sum of their probabilities. */
 typedef struct {
   const void* index;      /* [tokens, k] */
   const void* logit;      /* [tokens, k], the teacher's logits (or log-probabilities) */

@@ -107,3 +107,30 @@ def test_several_pieces_of_wide_heads(dtype, T, V, D, op):
     planes = 3 if dtype == "fp32" else 1
     if D > 1000:
         assert need < planes * 2 * V * D  # less than the whole weight: several pieces
+
+
+@pytest.mark.parametrize("T,dtype,op", [c for c in CASES if c[1] != "bf16"], ids=str)
+def test_captured_into_a_graph(T, dtype, op):
+    """Replays on two sets of inputs, with eager work and synchronizations between them,
+    give the eager calls' bits; which rows take part changes from one to the other."""
+    say(f"[case] graph {T} {dtype} {op}")
+    k = 0 if op == "xent" else 5
+    sets = [make(T, 1003, 128, dtype, seed=85 + i, ignored=0.2 + 0.5 * i, k=k) for i in (0, 1)]
+    want = [run(c, {}) for c in sets]
+    static = {name: x.clone() for name, x in sets[0].items()}
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        run(static, {})
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run(static, {})
+    for i in (0, 1, 0, 1, 1):
+        for name, x in sets[i].items():
+            static[name].copy_(x)
+        graph.replay()
+        torch.cuda.synchronize()
+        run(sets[1 - i], {})
+        for x, y in zip((out[0], out[1].lse, *out[2:]), (want[i][0], want[i][1].lse, *want[i][2:])):
+            assert torch.equal(x, y)
